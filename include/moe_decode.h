@@ -336,6 +336,117 @@ moe_status moe_lm_head_forward(const uint16_t* x_bf16, int32_t M, const uint8_t*
                                const float* scale, int32_t vocab, int32_t hidden,
                                float* logits, void* stream);
 
+/* ---- Around the expert layer ------------------------------------------------
+ * What stands between one expert layer's fp32 `out` and the next one's bf16
+ * `hidden`: the residual's addition with the RMS norm and an 8-bit output,
+ * routing by scores with a balance bias and groups, and an int8 matrix
+ * product for the dense projections and for the LM head at any token count.
+ * These calls take run-time sizes (nothing is compiled per shape), use no
+ * workspace, and keep the library's rules: dense row-major device tensors,
+ * every argument checked before anything is enqueued, nothing allocated or
+ * synchronised, sums in fixed orders.  Outputs may not overlap inputs or each
+ * other, except where a call says so (MOE_ERR_INVALID_ARG). */
+
+/* Types of a tensor given as `const void*` / `void*`. */
+typedef enum { MOE_TYPE_BF16 = 0, MOE_TYPE_F32 = 1 } moe_type;
+
+/* 8-bit codes of a row with one fp32 scale: s = amax / 448 (E4M3) or
+ * amax / 127 (int8), 1 for a row of zeros; codes of the correctly rounded
+ * quotient, to nearest even.  int8 codes lie in [-127, 127]. */
+typedef enum { MOE_QUANT_NONE = 0, MOE_QUANT_E4M3 = 1, MOE_QUANT_INT8 = 2 } moe_quant;
+
+/* Residual add, RMS norm and row quantisation of M rows of H elements:
+ *   r    = residual + x, added in fp32 and rounded to residual_type;
+ *   rstd = 1 / sqrt(mean(r^2) + eps), the sum in fp64, rounded to fp32;
+ *   y    = bf16((r * weight) * rstd), both products rounded to fp32;
+ *   q, scale = the 8-bit codes of y (of the bf16 values: with MOE_QUANT_E4M3
+ *          the codes and scales that moe_quant_act gives for y).
+ * x [M,H] of x_type (a layer's fp32 `out`, or bf16); residual [M,H] of
+ * residual_type, or NULL (r = x); weight [H] of weight_type.  Outputs:
+ * residual_out [M,H] of residual_type = r (may be `residual` itself),
+ * y bf16 [M,H], q u8/i8 [M,H] with scale fp32 [M]; each may be NULL (q and
+ * scale together, exactly when q_type is MOE_QUANT_NONE), not all of them.
+ * 1 <= H <= 32768; eps > 0 and finite.  x, residual, weight, residual_out, y
+ * and q are 16-byte aligned. */
+moe_status moe_add_rmsnorm(int32_t M, int32_t H, const void* x, int32_t x_type,
+                           const void* residual, int32_t residual_type,
+                           const void* weight, int32_t weight_type, double eps,
+                           void* residual_out, uint16_t* y,
+                           void* q, int32_t q_type, float* scale, void* stream);
+
+/* How moe_route_scores turns logits into scores. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+/* A router that chooses by scores.  num_experts 1..512, topk 1..8; the
+ * experts stand in num_groups (1..64) groups of equal size, of which
+ * group_topk stay; group_score (1 or 2): how many of a group's largest choice
+ * values are summed into the group's value; renormalise: nonzero divides the
+ * weights by their sum; factor multiplies them.  topk must not exceed
+ * group_topk * num_experts / num_groups. */
+typedef struct {
+    int32_t num_experts;
+    int32_t topk;
+    int32_t score;        /* moe_score */
+    int32_t num_groups;
+    int32_t group_topk;
+    int32_t group_score;
+    int32_t renormalise;
+    float   factor;
+} moe_router_params;
+
+/* Routing of M tokens by scores.  For a token's logits l (fp32, [M,E]):
+ *   s = sigmoid(l) or softmax(l) over all E, evaluated in fp64 and rounded to
+ *       fp32; c = s + bias (fp32 addition; bias fp32 [E] or NULL).
+ *   An expert whose logit is -inf or NaN, or whose c is -inf or NaN, is
+ *   unavailable to the token.  (A logit of +inf counts as the largest finite
+ *   fp32 value.)
+ *   Groups: a group's value is the sum of the group_score largest c among its
+ *   available experts (of one, if only one is; -inf if none is); the
+ *   group_topk groups of largest value stay.
+ *   topk_ids [M,K] = the K experts of the groups that stay with the largest
+ *   c, in that order; unavailable ones come last.  Ties go to the lowest
+ *   index, of groups and of experts.
+ *   topk_w [M,K] = s of those experts (not c), 0 for unavailable ones, divided
+ *   by their sum if renormalise (a sum of 0 leaves zeros), times factor.
+ * So ids are always distinct and in [0, E), and a token with no available
+ * expert has weights 0.  The scores are correctly rounded up to an fp64
+ * evaluation's error, so the ids do not depend on how a kernel sums or
+ * approximates. */
+moe_status moe_route_scores(const moe_router_params* router, int32_t M, const float* logits,
+                            const float* bias, int32_t* topk_ids, float* topk_w, void* stream);
+
+/* The router's logits [M,E] fp32 alone (a1 of moe_decode_forward, the same
+ * kernel), for moe_route_scores.  The checks of M and the shape are those of
+ * moe_route; no workspace. */
+moe_status moe_router_logits(const moe_shape* shape, int32_t M, const uint16_t* hidden,
+                             const uint16_t* router_w, float* logits, void* stream);
+
+/* The whole layer with routing by scores: router logits -> moe_route_scores
+ * -> the expert stages of moe_experts_forward_shared on the quantised hidden
+ * (the same kernels, so the same bits as the three calls).  shape's E and K
+ * must be the router's; bias and shared may be NULL. */
+moe_status moe_decode_forward_scored(const moe_shape* shape, const moe_router_params* router, int32_t M,
+                                     const uint16_t* hidden, const uint16_t* router_w, const float* bias,
+                                     const uint8_t* w13, const uint8_t* w13_scale,
+                                     const uint8_t* w2, const uint8_t* w2_scale,
+                                     const moe_shared_expert* shared,
+                                     float* out, void* ws, size_t ws_bytes, void* stream);
+
+/* int8 codes and scales (MOE_QUANT_INT8 above) of the rows of a bf16 matrix
+ * [rows, cols]: a weight's output channels at load time, or tokens.  q
+ * [rows, cols], scale [rows].  x_bf16 and q are 16-byte aligned. */
+moe_status moe_int8_quantize(const uint16_t* x_bf16, int32_t rows, int32_t cols, int8_t* q,
+                             float* scale, void* stream);
+
+/* out[m, n] = (sum_k a[m,k] * w[n,k]) * a_scale[m] * w_scale[n]: the product
+ * of int8 token rows a [M,K] with int8 output channels w [N,K], summed exactly
+ * in 32-bit integers, scaled in fp32 and rounded once to out_type; out [M,N].
+ * Any M, N > 0 and 1 <= K <= 131071 (beyond, a 32-bit sum of products could
+ * overflow).  Codes may be any int8 value.  a, w and out are 16-byte
+ * aligned. */
+moe_status moe_int8_linear(const int8_t* a, const float* a_scale, const int8_t* w, const float* w_scale,
+                           int32_t M, int32_t N, int32_t K, void* out, int32_t out_type, void* stream);
+
 /* Writes a one-line description of the kernels a call with this shape and M
  * would run (NUL-terminated, truncated to len).  Returns the same status the
  * call's shape validation would. */

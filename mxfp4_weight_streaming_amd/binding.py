@@ -55,6 +55,12 @@ class MoeSharedExpert(ctypes.Structure):
                 ("w2_scale", ctypes.c_void_p)]
 
 
+class MoeRouterParams(ctypes.Structure):
+    _fields_ = [("num_experts", ctypes.c_int32), ("topk", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("num_groups", ctypes.c_int32), ("group_topk", ctypes.c_int32), ("group_score", ctypes.c_int32),
+                ("renormalise", ctypes.c_int32), ("factor", ctypes.c_float)]
+
+
 class MoeJitReport(ctypes.Structure):
     _fields_ = [("from_cache", ctypes.c_int32), ("has_chunk_path", ctypes.c_int32), ("has_lm_head", ctypes.c_int32),
                 ("num_kernels", ctypes.c_int32), ("seconds", ctypes.c_double), ("cache_file", ctypes.c_char * 1024)]
@@ -70,6 +76,7 @@ _S = ctypes.POINTER(MoeShape)
 _SH = ctypes.POINTER(MoeSharedExpert)
 _i32 = ctypes.c_int32
 _sz = ctypes.c_size_t
+_RP = ctypes.POINTER(MoeRouterParams)
 
 _SIGNATURES = {
     "moe_workspace_bytes": (_sz, [_S, _i32]),
@@ -91,6 +98,13 @@ _SIGNATURES = {
     "moe_fp8_encode_range": (ctypes.c_int, [ctypes.c_uint32, ctypes.c_int64, _V, _V]),
     "moe_lm_head_quantize": (ctypes.c_int, [_V, _i32, _i32, _V, _V, _V]),
     "moe_lm_head_forward": (ctypes.c_int, [_V, _i32, _V, _V, _i32, _i32, _V, _V]),
+    "moe_add_rmsnorm": (ctypes.c_int, [_i32, _i32, _V, _i32, _V, _i32, _V, _i32, ctypes.c_double, _V, _V, _V, _i32,
+                                       _V, _V]),
+    "moe_route_scores": (ctypes.c_int, [_RP, _i32, _V, _V, _V, _V, _V]),
+    "moe_router_logits": (ctypes.c_int, [_S, _i32, _V, _V, _V, _V]),
+    "moe_decode_forward_scored": (ctypes.c_int, [_S, _RP, _i32, _V, _V, _V, _V, _V, _V, _V, _SH, _V, _V, _sz, _V]),
+    "moe_int8_quantize": (ctypes.c_int, [_V, _i32, _i32, _V, _V, _V]),
+    "moe_int8_linear": (ctypes.c_int, [_V, _V, _V, _V, _i32, _i32, _i32, _V, _i32, _V]),
     "moe_path_info": (ctypes.c_int, [_S, _i32, ctypes.c_char_p, _sz]),
     "moe_jit_build": (ctypes.c_int, [_S, ctypes.c_char_p, ctypes.c_char_p, ctypes.POINTER(MoeJitReport)]),
     "moe_jit_load": (ctypes.c_int, [_S, ctypes.c_char_p, _i32, ctypes.POINTER(MoeJitReport)]),
@@ -296,6 +310,147 @@ def moe_lm_head_forward(x_bf16, q, scale, logits, stream=None):
     V = q.shape[0]
     _check(_lib.moe_lm_head_forward(_p(x_bf16), M, _p(q), _p(scale), V, H, _p(logits), _stream(stream)),
            "moe_lm_head_forward")
+
+
+# ---- around the expert layer --------------------------------------------------
+# These calls take sizes and types from the tensors, so they check them: each
+# tensor dense, on the current device, of a type the call knows.  bf16 data may
+# also come as int16 / uint16 bits, E4M3 codes as uint8.
+TYPE_BF16, TYPE_F32 = 0, 1
+QUANT_NONE, QUANT_E4M3, QUANT_INT8 = 0, 1, 2
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+_float_types = None     # torch dtype -> moe_type, made at the first call (torch is imported lazily)
+_code_types = None      # torch dtype -> moe_quant
+
+
+def _types():
+    global _float_types, _code_types
+    if _float_types is None:
+        import torch
+        _code_types = {torch.float8_e4m3fn: QUANT_E4M3, torch.uint8: QUANT_E4M3, torch.int8: QUANT_INT8}
+        _float_types = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16, torch.int16: TYPE_BF16,
+                        torch.uint16: TYPE_BF16}
+    return _float_types, _code_types
+
+
+def _dense(name, t, shape, types, want):
+    """The type tag of tensor t, checked: its shape, dense, its dtype one of `types`."""
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, {tuple(shape)} is needed")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+    tag = types.get(t.dtype)
+    if tag is None or (want is not None and tag != want):
+        raise ValueError(f"{name} has type {t.dtype}, which this call does not take")
+    return tag
+
+
+def _f32(name, t, n):
+    """A dense fp32 tensor of n elements, or None."""
+    if t is not None and (t.numel() != n or not t.is_contiguous() or _types()[0].get(t.dtype) != TYPE_F32):
+        raise ValueError(f"{name} must be a contiguous float32 tensor of {n} elements")
+
+
+def _on_current_device(*tensors):
+    """Every tensor on torch's current device: kernels are launched there."""
+    import torch
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+
+
+def moe_add_rmsnorm(x, residual, weight, eps, residual_out, y=None, q=None, scale=None, stream=None):
+    """residual_out = residual + x; y = its RMS norm times weight in bf16; q, scale = y's 8-bit codes.
+
+    x [M,H] float32 or bf16; residual [M,H] float32 or bf16, or None (then residual_out gives the type, else x's);
+    weight [H] float32 or bf16.  residual_out (may be residual), y and (q, scale) may each be None; q's dtype
+    chooses the codes: float8_e4m3fn or uint8 for E4M3, int8 for int8."""
+    floats, codes = _types()
+    M, H = shp = x.shape
+    x_type = _dense("x", x, shp, floats, None)
+    r_type = x_type
+    if residual is not None:
+        r_type = _dense("residual", residual, shp, floats, None)
+        if residual_out is not None:
+            _dense("residual_out", residual_out, shp, floats, r_type)
+    elif residual_out is not None:
+        r_type = _dense("residual_out", residual_out, shp, floats, None)
+    w_type = _dense("weight", weight, shp[1:], floats, None)
+    if y is not None:
+        _dense("y", y, shp, floats, TYPE_BF16)
+    q_type = QUANT_NONE if q is None else _dense("q", q, shp, codes, None)
+    _f32("scale", scale, M)
+    _on_current_device(x, residual, weight, residual_out, y, q, scale)
+    _check(_lib.moe_add_rmsnorm(M, H, _p(x), x_type, _p(residual), r_type, _p(weight), w_type, eps, _p(residual_out),
+                                _p(y), _p(q), q_type, _p(scale), _stream(stream)),
+           "moe_add_rmsnorm")
+
+
+def router(num_experts: int, topk: int, score: str = "sigmoid", groups: int = 1, group_topk: int = 1,
+           group_score: int = 2, renormalise: bool = True, factor: float = 1.0) -> MoeRouterParams:
+    """A router that chooses by scores, for moe_route_scores and moe_decode_forward_scored."""
+    if score not in SCORES:
+        raise ValueError(f"score {score!r} is none of {sorted(SCORES)}")
+    return MoeRouterParams(num_experts, topk, SCORES[score], groups, group_topk, group_score, int(renormalise), factor)
+
+
+def moe_route_scores(rp: MoeRouterParams, logits, bias, topk_ids, topk_w, stream=None):
+    """topk_ids [M,K] int32 and topk_w [M,K] float32 of logits [M,E] float32; bias [E] float32 or None."""
+    M = logits.shape[0]
+    _f32("logits", logits, M * rp.num_experts)
+    _f32("bias", bias, rp.num_experts)
+    _f32("topk_w", topk_w, M * rp.topk)
+    if topk_ids.numel() != M * rp.topk or topk_ids.element_size() != 4 or topk_ids.is_floating_point() \
+            or not topk_ids.is_contiguous():
+        raise ValueError(f"topk_ids must be a contiguous int32 tensor of {M * rp.topk} elements")
+    _on_current_device(logits, bias, topk_ids, topk_w)
+    _check(_lib.moe_route_scores(ctypes.byref(rp), M, _p(logits), _p(bias), _p(topk_ids), _p(topk_w),
+                                 _stream(stream)),
+           "moe_route_scores")
+
+
+def moe_router_logits(shp, M, hidden, router_w, logits, stream=None):
+    _check(_lib.moe_router_logits(ctypes.byref(shp), M, _p(hidden), _p(router_w), _p(logits), _stream(stream)),
+           "moe_router_logits")
+
+
+def moe_decode_forward_scored(shp, rp, M, hidden, router_w, bias, w13, w13_scale, w2, w2_scale, out, ws, shared=None,
+                              stream=None):
+    """The layer with routing by scores (rp from router()); shared as in moe_decode_forward_shared."""
+    sh = _shared(shared)
+    _check(_lib.moe_decode_forward_scored(ctypes.byref(shp), ctypes.byref(rp), M, _p(hidden), _p(router_w), _p(bias),
+                                          _p(w13), _p(w13_scale), _p(w2), _p(w2_scale),
+                                          ctypes.byref(sh) if sh is not None else None, _p(out), _p(ws), _nbytes(ws),
+                                          _stream(stream)),
+           "moe_decode_forward_scored")
+
+
+def moe_int8_quantize(x_bf16, q, scale, stream=None):
+    """x_bf16 [rows, cols] -> int8 codes q [rows, cols] and scale [rows]."""
+    floats, codes = _types()
+    rows, cols = x_bf16.shape
+    _dense("x_bf16", x_bf16, x_bf16.shape, floats, TYPE_BF16)
+    _dense("q", q, x_bf16.shape, codes, QUANT_INT8)
+    _f32("scale", scale, rows)
+    _on_current_device(x_bf16, q, scale)
+    _check(_lib.moe_int8_quantize(_p(x_bf16), rows, cols, _p(q), _p(scale), _stream(stream)), "moe_int8_quantize")
+
+
+def moe_int8_linear(a, a_scale, w, w_scale, out, stream=None):
+    """out [M,N] (float32 or bf16) = (a [M,K] int8 times w [N,K] int8 transposed) * a_scale [M] * w_scale [N]."""
+    floats, codes = _types()
+    M, K = a.shape
+    N = w.shape[0]
+    _dense("a", a, (M, K), codes, QUANT_INT8)
+    _dense("w", w, (N, K), codes, QUANT_INT8)
+    out_type = _dense("out", out, (M, N), floats, None)
+    _f32("a_scale", a_scale, M)
+    _f32("w_scale", w_scale, N)
+    _on_current_device(a, a_scale, w, w_scale, out)
+    _check(_lib.moe_int8_linear(_p(a), _p(a_scale), _p(w), _p(w_scale), M, N, K, _p(out), out_type, _stream(stream)),
+           "moe_int8_linear")
 
 
 def _path_arg(p):

@@ -1,6 +1,7 @@
 // moe_api.hip -- the C ABI declared in include/moe_decode.h: argument
 // validation, workspace carving and launch ordering on the caller's stream.
 // Nothing here allocates, frees or synchronises.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
@@ -454,6 +455,94 @@ moe_status experts_forward(const moe_shape* shape, int32_t M, const uint8_t* act
     return enqueue_down(shape, M, h, nullptr, nullptr, q2_tap, s2_tap, topk_w, w2, w2_scale, out, c, s, {}, sh);
 }
 
+// ---- operators around the expert layer ---------------------------------------
+struct Range {
+    const void* p;
+    size_t bytes;
+    const char* name;
+};
+
+// Whether two buffers (either may be NULL) share a byte.
+bool overlap(const Range& a, const Range& b)
+{
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    return a.p != nullptr && b.p != nullptr && x < y + b.bytes && y < x + a.bytes;
+}
+
+// Outputs share no byte with an input or with each other.
+template <int NI, int NO>
+moe_status check_apart(const Range (&in)[NI], const Range (&out)[NO])
+{
+    for (int o = 0; o < NO; ++o) {
+        for (int i = 0; i < NI; ++i)
+            if (overlap(out[o], in[i]))
+                return fail(MOE_ERR_INVALID_ARG, "%s overlaps %s", out[o].name, in[i].name);
+        for (int i = 0; i < o; ++i)
+            if (overlap(out[o], out[i]))
+                return fail(MOE_ERR_INVALID_ARG, "%s overlaps %s", out[o].name, out[i].name);
+    }
+    return MOE_OK;
+}
+
+bool type_ok(int32_t t) { return t == MOE_TYPE_BF16 || t == MOE_TYPE_F32; }
+size_t type_bytes(int32_t t) { return t == MOE_TYPE_F32 ? 4 : 2; }
+bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+
+#define CHECK_ALIGN4(p)                                                                        \
+    do {                                                                                       \
+        if (!aligned4(p)) return fail(MOE_ERR_ALIGNMENT, "%s is not 4-byte aligned", #p);      \
+    } while (0)
+
+moe_status check_router(const moe_router_params* r)
+{
+    if (r == nullptr) return fail(MOE_ERR_INVALID_ARG, "router is NULL");
+    const int E = r->num_experts, K = r->topk, G = r->num_groups;
+    if (E <= 0 || K <= 0 || G <= 0)
+        return fail(MOE_ERR_INVALID_ARG, "router has a non-positive size (E=%d K=%d groups=%d)", E, K, G);
+    if (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID)
+        return fail(MOE_ERR_INVALID_ARG, "score %d is neither softmax (0) nor sigmoid (1)", r->score);
+    if (E % G != 0) return fail(MOE_ERR_INVALID_ARG, "E (%d) does not split into %d groups of equal size", E, G);
+    if (r->group_topk < 1 || r->group_topk > G)
+        return fail(MOE_ERR_INVALID_ARG, "group_topk (%d) is not in 1..%d", r->group_topk, G);
+    if (r->group_score != 1 && r->group_score != 2)
+        return fail(MOE_ERR_INVALID_ARG, "group_score (%d) is neither 1 nor 2", r->group_score);
+    if (K > r->group_topk * (E / G))
+        return fail(MOE_ERR_INVALID_ARG, "K (%d) exceeds the %d experts of %d groups", K, r->group_topk * (E / G),
+                    r->group_topk);
+    if (!isfinite(r->factor)) return fail(MOE_ERR_INVALID_ARG, "factor is not finite");
+    if (E > moe::kMaxExperts)
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "E (%d) above %d is not compiled", E, moe::kMaxExperts);
+    if (K > moe::kMaxTopK) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "K (%d) above %d is not compiled", K, moe::kMaxTopK);
+    if (G > moe::kMaxGroups)
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%d groups, above %d, are not compiled", G, moe::kMaxGroups);
+    return MOE_OK;
+}
+
+moe_status enqueue_route_scores(const moe_router_params* r, int32_t M, const float* logits, const float* bias,
+                                int32_t* ids, float* w, hipStream_t st)
+{
+    moe::ScoreArgs a{logits, bias, ids, w, M, r->num_experts, r->topk, r->score, r->num_groups, r->group_topk,
+                     r->group_score, r->renormalise != 0 ? 1 : 0, r->factor};
+    hipError_t e = moe::launch_route_scores(a, st);
+    return e == hipSuccess ? MOE_OK : hip_fail(e, "route_scores launch");
+}
+
+// Router logits into `logits`; at M <= 8 with act_q also the FP8 activations
+// (the same kernel), otherwise the caller enqueues the quantisation.
+moe_status enqueue_logits(const moe_shape* s, int32_t M, const uint16_t* x, const uint16_t* wr, float* logits,
+                          uint8_t* act_q, float* act_s, hipStream_t st)
+{
+    hipError_t e;
+    if (chunked(M)) {
+        moe::ChunkRouterArgs a{x, wr, M, s->num_experts, logits};
+        e = moe::launch_chunk_router(s->hidden, a, st);
+    } else {
+        moe::RouterArgs a{x, wr, M, s->num_experts, logits, act_q, act_s};
+        e = moe::launch_router(s->hidden, token_bound(M), a, st);
+    }
+    return e == hipSuccess ? MOE_OK : hip_fail(e, "router launch");
+}
+
 // ---- the entry point that allocates nothing --------------------------------
 // A workspace that lives in the library itself: one file-scope device array,
 // of which every GPU that loads the library holds its own copy until the
@@ -710,6 +799,144 @@ moe_status moe_fp8_encode_range(uint32_t first_bits, int64_t n, uint8_t* q, void
     if (n < 0) return fail(MOE_ERR_INVALID_ARG, "n (%lld) is negative", (long long)n);
     hipError_t e = moe::launch_fp8_encode_range(first_bits, n, q, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? MOE_OK : hip_fail(e, "fp8 encode launch");
+}
+
+moe_status moe_add_rmsnorm(int32_t M, int32_t H, const void* x, int32_t x_type, const void* residual,
+                           int32_t residual_type, const void* weight, int32_t weight_type, double eps,
+                           void* residual_out, uint16_t* y, void* q, int32_t q_type, float* scale, void* stream)
+{
+    CHECK_PTR(x); CHECK_PTR(weight);
+    if (M <= 0 || H <= 0) return fail(MOE_ERR_INVALID_ARG, "M (%d) and H (%d) must be positive", M, H);
+    if (!type_ok(x_type) || !type_ok(residual_type) || !type_ok(weight_type))
+        return fail(MOE_ERR_INVALID_ARG, "a type is neither bf16 (0) nor fp32 (1): x %d, residual %d, weight %d", x_type,
+                    residual_type, weight_type);
+    if (q_type != MOE_QUANT_NONE && q_type != MOE_QUANT_E4M3 && q_type != MOE_QUANT_INT8)
+        return fail(MOE_ERR_INVALID_ARG, "q_type %d is none of 0 (none), 1 (E4M3), 2 (int8)", q_type);
+    if ((q != nullptr) != (q_type != MOE_QUANT_NONE) || (scale != nullptr) != (q_type != MOE_QUANT_NONE))
+        return fail(MOE_ERR_INVALID_ARG, "q and scale go together with a q_type, and are NULL without one");
+    if (residual_out == nullptr && y == nullptr && q == nullptr)
+        return fail(MOE_ERR_INVALID_ARG, "residual_out, y and q are all NULL");
+    if (!(eps > 0.0) || !isfinite(eps)) return fail(MOE_ERR_INVALID_ARG, "eps must be positive and finite");
+    if (H > moe::kMaxNormHidden)
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "H=%d above %d is not compiled", H, moe::kMaxNormHidden);
+    CHECK_ALIGN(x); CHECK_ALIGN(residual); CHECK_ALIGN(weight); CHECK_ALIGN(residual_out); CHECK_ALIGN(y);
+    CHECK_ALIGN(q); CHECK_ALIGN4(scale);
+    const size_t n = (size_t)M * H;
+    const Range in[] = {{x, n * type_bytes(x_type), "x"},
+                        {weight, (size_t)H * type_bytes(weight_type), "weight"},
+                        {residual == residual_out ? nullptr : residual, n * type_bytes(residual_type), "residual"}};
+    const Range out[] = {{residual_out, n * type_bytes(residual_type), "residual_out"},
+                         {y, n * 2, "y"},
+                         {q, n, "q"},
+                         {scale, (size_t)M * 4, "scale"}};
+    const moe_status st = check_apart(in, out);
+    if (st != MOE_OK) return st;
+    moe::NormArgs a{x, residual, weight, residual_out, y, static_cast<uint8_t*>(q), scale, eps, M, H, x_type,
+                    residual_type, weight_type, q_type};
+    hipError_t e = moe::launch_add_rmsnorm(a, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? MOE_OK : hip_fail(e, "add_rmsnorm launch");
+}
+
+moe_status moe_route_scores(const moe_router_params* router, int32_t M, const float* logits, const float* bias,
+                            int32_t* topk_ids, float* topk_w, void* stream)
+{
+    moe_status st = check_router(router);
+    if (st != MOE_OK) return st;
+    if (M <= 0) return fail(MOE_ERR_INVALID_ARG, "M (%d) must be positive", M);
+    CHECK_PTR(logits); CHECK_PTR(topk_ids); CHECK_PTR(topk_w);
+    CHECK_ALIGN(logits); CHECK_ALIGN(bias); CHECK_ALIGN4(topk_ids); CHECK_ALIGN4(topk_w);
+    const size_t pairs = (size_t)M * router->topk * 4;
+    const Range in[] = {{logits, (size_t)M * router->num_experts * 4, "logits"},
+                        {bias, (size_t)router->num_experts * 4, "bias"}};
+    const Range out[] = {{topk_ids, pairs, "topk_ids"}, {topk_w, pairs, "topk_w"}};
+    if ((st = check_apart(in, out)) != MOE_OK) return st;
+    return enqueue_route_scores(router, M, logits, bias, topk_ids, topk_w, static_cast<hipStream_t>(stream));
+}
+
+moe_status moe_router_logits(const moe_shape* shape, int32_t M, const uint16_t* hidden, const uint16_t* router_w,
+                             float* logits, void* stream)
+{
+    moe_status st = check_shape(shape, M);
+    if (st != MOE_OK) return st;
+    CHECK_PTR(hidden); CHECK_PTR(router_w); CHECK_PTR(logits);
+    CHECK_ALIGN(hidden); CHECK_ALIGN(router_w); CHECK_ALIGN(logits);
+    const Range in[] = {{hidden, (size_t)M * shape->hidden * 2, "hidden"},
+                        {router_w, (size_t)shape->num_experts * shape->hidden * 2, "router_w"}};
+    const Range out[] = {{logits, (size_t)M * shape->num_experts * 4, "logits"}};
+    if ((st = check_apart(in, out)) != MOE_OK) return st;
+    return enqueue_logits(shape, M, hidden, router_w, logits, nullptr, nullptr, static_cast<hipStream_t>(stream));
+}
+
+moe_status moe_decode_forward_scored(const moe_shape* shape, const moe_router_params* router, int32_t M,
+                                     const uint16_t* hidden, const uint16_t* router_w, const float* bias,
+                                     const uint8_t* w13, const uint8_t* w13_scale, const uint8_t* w2,
+                                     const uint8_t* w2_scale, const moe_shared_expert* shared, float* out, void* ws,
+                                     size_t ws_bytes, void* stream)
+{
+    moe_status st = check_shape(shape, M);
+    if (st != MOE_OK) return st;
+    if ((st = check_router(router)) != MOE_OK) return st;
+    if (router->num_experts != shape->num_experts || router->topk != shape->topk)
+        return fail(MOE_ERR_INVALID_ARG, "the router has E=%d K=%d, the shape E=%d K=%d", router->num_experts,
+                    router->topk, shape->num_experts, shape->topk);
+    CHECK_PTR(hidden); CHECK_PTR(router_w); CHECK_PTR(w13); CHECK_PTR(w13_scale);
+    CHECK_PTR(w2); CHECK_PTR(w2_scale); CHECK_PTR(out);
+    CHECK_ALIGN(hidden); CHECK_ALIGN(router_w); CHECK_ALIGN(bias); CHECK_ALIGN(w13); CHECK_ALIGN(w2); CHECK_ALIGN(out);
+    if ((st = check_shared(shared)) != MOE_OK) return st;
+    if ((st = check_ws(shape, M, ws, ws_bytes)) != MOE_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    // the expert stages leave these parts of the workspace alone when the
+    // routing and the codes are given
+    const Carved c = carve(shape, M, ws);
+    float* logits = c.at<float>(c.L.logits);
+    int32_t* ids = c.at<int32_t>(c.L.ids);
+    float* w = c.at<float>(c.L.w);
+    uint8_t* q = c.at<uint8_t>(c.L.act_q);
+    float* sc = c.at<float>(c.L.act_s);
+    if ((st = enqueue_logits(shape, M, hidden, router_w, logits, q, sc, s)) != MOE_OK) return st;
+    if (chunked(M) && (st = enqueue_quant(shape, M, hidden, q, sc, s)) != MOE_OK) return st;
+    if ((st = enqueue_route_scores(router, M, logits, bias, ids, w, s)) != MOE_OK) return st;
+    return experts_forward(shape, M, q, sc, ids, w, w13, w13_scale, w2, w2_scale, shared, out, nullptr, ws, ws_bytes,
+                           stream);
+}
+
+moe_status moe_int8_quantize(const uint16_t* x_bf16, int32_t rows, int32_t cols, int8_t* q, float* scale, void* stream)
+{
+    CHECK_PTR(x_bf16); CHECK_PTR(q); CHECK_PTR(scale);
+    if (rows <= 0 || cols <= 0)
+        return fail(MOE_ERR_INVALID_ARG, "rows (%d) and cols (%d) must be positive", rows, cols);
+    CHECK_ALIGN(x_bf16); CHECK_ALIGN(q); CHECK_ALIGN4(scale);
+    const size_t n = (size_t)rows * cols;
+    const Range in[] = {{x_bf16, n * 2, "x_bf16"}};
+    const Range out[] = {{q, n, "q"}, {scale, (size_t)rows * 4, "scale"}};
+    const moe_status st = check_apart(in, out);
+    if (st != MOE_OK) return st;
+    hipError_t e = moe::launch_int8_quantize(x_bf16, rows, cols, reinterpret_cast<uint8_t*>(q), scale,
+                                             static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? MOE_OK : hip_fail(e, "int8 quantisation launch");
+}
+
+moe_status moe_int8_linear(const int8_t* a, const float* a_scale, const int8_t* w, const float* w_scale, int32_t M,
+                           int32_t N, int32_t K, void* out, int32_t out_type, void* stream)
+{
+    CHECK_PTR(a); CHECK_PTR(a_scale); CHECK_PTR(w); CHECK_PTR(w_scale); CHECK_PTR(out);
+    if (M <= 0 || N <= 0 || K <= 0)
+        return fail(MOE_ERR_INVALID_ARG, "M (%d), N (%d) and K (%d) must be positive", M, N, K);
+    if (!type_ok(out_type)) return fail(MOE_ERR_INVALID_ARG, "out_type %d is neither bf16 (0) nor fp32 (1)", out_type);
+    if (K > moe::kMaxInt8Depth)
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "K=%d above %d: a 32-bit sum could overflow", K, moe::kMaxInt8Depth);
+    CHECK_ALIGN(a); CHECK_ALIGN(w); CHECK_ALIGN(out); CHECK_ALIGN4(a_scale); CHECK_ALIGN4(w_scale);
+    const Range in[] = {{a, (size_t)M * K, "a"},
+                        {w, (size_t)N * K, "w"},
+                        {a_scale, (size_t)M * 4, "a_scale"},
+                        {w_scale, (size_t)N * 4, "w_scale"}};
+    const Range o[] = {{out, (size_t)M * N * type_bytes(out_type), "out"}};
+    const moe_status st = check_apart(in, o);
+    if (st != MOE_OK) return st;
+    moe::Int8Args g{reinterpret_cast<const uint8_t*>(a), reinterpret_cast<const uint8_t*>(w), a_scale, w_scale, out,
+                    M, N, K, out_type};
+    hipError_t e = moe::launch_int8_linear(g, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? MOE_OK : hip_fail(e, "int8 product launch");
 }
 
 moe_status moe_path_info(const moe_shape* shape, int32_t M, char* buf, size_t len)

@@ -10,6 +10,7 @@
 
 #include <string>
 
+#include "around_types.hpp"
 #include "moe_types.hpp"
 
 namespace moe {
@@ -120,6 +121,13 @@ bool lm_head_shape_supported(int H);
 hipError_t launch_lm_head_quant(const uint16_t* w, int V, int H, uint8_t* q, float* scale, hipStream_t s);
 hipError_t launch_lm_head_gemv(int H, int mt, const uint16_t* x, int M, const uint8_t* q, const float* scale, int V,
                                float* logits, hipStream_t s);
+
+// Operators around the expert layer (norm.hip, route_scores.hip,
+// int8_linear.hip): run-time sizes, no workspace.
+hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t s);
+hipError_t launch_route_scores(const ScoreArgs& a, hipStream_t s);
+hipError_t launch_int8_quantize(const uint16_t* x, int rows, int cols, uint8_t* q, float* scale, hipStream_t s);
+hipError_t launch_int8_linear(const Int8Args& a, hipStream_t s);
 
 // Run-time compilation of the shape-templated kernels (jit.hip).
 enum class JitStatus { Ok, BadShape, BadArch, CacheIo, Compile, Load };
