@@ -46,6 +46,7 @@ struct Int8Args {
     void* out;             // [M,N]
     int64_t M, N;
     int K, out_type;
+    int xm;                // tile kernels: parts along the tokens, of 8 (1, 2, 4 or 8)
 };
 
 }  // namespace moe

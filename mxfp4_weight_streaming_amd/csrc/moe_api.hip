@@ -934,7 +934,7 @@ moe_status moe_int8_linear(const int8_t* a, const float* a_scale, const int8_t* 
     const moe_status st = check_apart(in, o);
     if (st != MOE_OK) return st;
     moe::Int8Args g{reinterpret_cast<const uint8_t*>(a), reinterpret_cast<const uint8_t*>(w), a_scale, w_scale, out,
-                    M, N, K, out_type};
+                    M, N, K, out_type, 1};
     hipError_t e = moe::launch_int8_linear(g, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? MOE_OK : hip_fail(e, "int8 product launch");
 }
