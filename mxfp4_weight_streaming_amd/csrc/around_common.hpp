@@ -30,14 +30,29 @@ __device__ __forceinline__ double row_lane_f64(double v, int lane)
     return __builtin_bit_cast(double, read_lane_u64(__builtin_bit_cast(uint64_t, v), lane));
 }
 
-// Wave-wide sum in a fixed order; every lane gets it.
-__device__ __forceinline__ double wave_sum_f64(double v)
+// Sum over each row of 16 lanes, and over the wave, in a fixed order; every lane
+// gets it.
+__device__ __forceinline__ double row_sum_f64(double v)
 {
     v += dpp_f64<kDppXor1>(v);
     v += dpp_f64<kDppXor2>(v);
     v += dpp_f64<kDppHalfMirror>(v);
-    v += dpp_f64<kDppMirror>(v);
+    return v + dpp_f64<kDppMirror>(v);
+}
+
+__device__ __forceinline__ double wave_sum_f64(double v)
+{
+    v = row_sum_f64(v);
     return (row_lane_f64(v, 0) + row_lane_f64(v, 16)) + (row_lane_f64(v, 32) + row_lane_f64(v, 48));
+}
+
+// Largest unsigned value of each row of 16 lanes.
+__device__ __forceinline__ uint32_t row_max_u32(uint32_t v)
+{
+    v = max(v, dpp_u32<kDppXor1>(v));
+    v = max(v, dpp_u32<kDppXor2>(v));
+    v = max(v, dpp_u32<kDppHalfMirror>(v));
+    return max(v, dpp_u32<kDppMirror>(v));
 }
 
 }  // namespace moe
