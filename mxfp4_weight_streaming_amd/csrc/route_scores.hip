@@ -10,8 +10,20 @@ namespace moe {
 
 hipError_t launch_route_scores(const ScoreArgs& a, hipStream_t s)
 {
-    const dim3 grid((unsigned)std::min<int64_t>((a.M + 3) / 4, (int64_t)1 << 20));
-    hipLaunchKernelGGL(route_scores_kernel, grid, dim3(256), 0, s, a);
+    // workgroups of 4 waves, one token a wave; about as many as the chip holds at
+    // once, each striding over the tokens with the next token's logits in flight
+    const dim3 grid((unsigned)std::min<int64_t>((a.M + 3) / 4, 2048)), block(256);
+    const bool softmax = a.score == kScoreSoftmax;
+#define MOE_ROUTE_SCORES(PER)                                                                             \
+    do {                                                                                                  \
+        if (softmax) hipLaunchKernelGGL((route_scores_kernel<PER, true>), grid, block, 0, s, a);          \
+        else hipLaunchKernelGGL((route_scores_kernel<PER, false>), grid, block, 0, s, a);                 \
+    } while (0)
+    if (a.E <= 64) MOE_ROUTE_SCORES(1);
+    else if (a.E <= 128) MOE_ROUTE_SCORES(2);
+    else if (a.E <= 256) MOE_ROUTE_SCORES(4);
+    else MOE_ROUTE_SCORES(8);
+#undef MOE_ROUTE_SCORES
     return hipGetLastError();
 }
 
