@@ -149,10 +149,27 @@ def _p(t):
     return t.data_ptr()
 
 
+_current = None     # (current device, current stream's handle on a device), made at the first call
+
+
+def _torch_current():
+    """torch's current device and stream handles.  torch.cuda.current_stream() makes a Stream object, 2.8 us a call,
+    as long as a kernel launch; torch's own compiled callers ask for the handle alone, 0.1 us."""
+    global _current
+    if _current is None:
+        import torch
+        torch.cuda.init()
+        device, stream = getattr(torch._C, "_cuda_getDevice", None), getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if device is None or stream is None:
+            device, stream = torch.cuda.current_device, lambda d: torch.cuda.current_stream(d).cuda_stream
+        _current = device, stream
+    return _current
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        device, handle = _current or _torch_current()
+        return handle(device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -320,45 +337,64 @@ TYPE_BF16, TYPE_F32 = 0, 1
 QUANT_NONE, QUANT_E4M3, QUANT_INT8 = 0, 1, 2
 SCORES = {"softmax": 0, "sigmoid": 1}
 
-_float_types = None     # torch dtype -> moe_type, made at the first call (torch is imported lazily)
-_code_types = None      # torch dtype -> moe_quant
+_type_tags = None     # made at the first call (torch is imported lazily)
 
 
 def _types():
-    global _float_types, _code_types
-    if _float_types is None:
+    """torch dtypes and their tags: of floats (moe_type), of codes (moe_quant), of bf16 alone, of float32 alone."""
+    global _type_tags
+    if _type_tags is None:
         import torch
-        _code_types = {torch.float8_e4m3fn: QUANT_E4M3, torch.uint8: QUANT_E4M3, torch.int8: QUANT_INT8}
-        _float_types = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16, torch.int16: TYPE_BF16,
-                        torch.uint16: TYPE_BF16}
-    return _float_types, _code_types
+        bf16 = {torch.bfloat16: TYPE_BF16, torch.int16: TYPE_BF16, torch.uint16: TYPE_BF16}
+        f32 = {torch.float32: TYPE_F32}
+        _type_tags = ({**f32, **bf16},
+                      {torch.float8_e4m3fn: QUANT_E4M3, torch.uint8: QUANT_E4M3, torch.int8: QUANT_INT8}, bf16, f32)
+    return _type_tags
 
 
-def _dense(name, t, shape, types, want):
-    """The type tag of tensor t, checked: its shape, dense, its dtype one of `types`."""
-    if t.shape != shape:
+_int_types = None
+
+
+def _ints():
+    """torch dtypes of int32 data, and of int8 codes."""
+    global _int_types
+    if _int_types is None:
+        import torch
+        _int_types = {torch.int32: 0, torch.uint32: 0}, {torch.int8: 0}
+    return _int_types
+
+
+def _refuse(name, t, shape, types, device):
+    if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, {tuple(shape)} is needed")
     if not t.is_contiguous():
         raise ValueError(f"{name} is not contiguous")
-    tag = types.get(t.dtype)
-    if tag is None or (want is not None and tag != want):
+    if t.dtype not in types:
         raise ValueError(f"{name} has type {t.dtype}, which this call does not take")
+    raise ValueError(f"{name} is on {t.device}, another tensor on device {device}")
+
+
+def _tag(name, t, shape, types, device):
+    """The type tag of tensor t, checked: its shape, dense, its dtype one of `types`, its device."""
+    tag = types.get(t.dtype)
+    if tag is None or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        _refuse(name, t, shape, types, device)
     return tag
 
 
-def _f32(name, t, n):
-    """A dense fp32 tensor of n elements, or None."""
-    if t is not None and (t.numel() != n or not t.is_contiguous() or _types()[0].get(t.dtype) != TYPE_F32):
-        raise ValueError(f"{name} must be a contiguous float32 tensor of {n} elements")
+def _vector(name, t, n, types, device):
+    """The same for n elements in any shape."""
+    if t.dtype not in types or t.numel() != n or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{name} must be a contiguous tensor of {n} elements of {' or '.join(map(str, types))} on the "
+                         f"other tensors' device; it has {t.numel()} of {t.dtype} on {t.device}")
 
 
-def _on_current_device(*tensors):
-    """Every tensor on torch's current device: kernels are launched there."""
-    import torch
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+def _stream_on(device, stream):
+    """The stream's handle; the tensors' device must be torch's current one, where kernels are launched."""
+    current, handle = _current or _torch_current()
+    if device != current():
+        raise ValueError(f"the tensors are on device {device}, the current device is {current()}")
+    return handle(device) if stream is None else _stream(stream)
 
 
 def moe_add_rmsnorm(x, residual, weight, eps, residual_out, y=None, q=None, scale=None, stream=None):
@@ -367,24 +403,35 @@ def moe_add_rmsnorm(x, residual, weight, eps, residual_out, y=None, q=None, scal
     x [M,H] float32 or bf16; residual [M,H] float32 or bf16, or None (then residual_out gives the type, else x's);
     weight [H] float32 or bf16.  residual_out (may be residual), y and (q, scale) may each be None; q's dtype
     chooses the codes: float8_e4m3fn or uint8 for E4M3, int8 for int8."""
-    floats, codes = _types()
-    M, H = shp = x.shape
-    x_type = _dense("x", x, shp, floats, None)
-    r_type = x_type
+    floats, codes, bf16, f32 = _types()
+    shape = x.shape
+    M, H = shape
+    dev = x.get_device()
+    r_type = x_type = _tag("x", x, shape, floats, dev)
+    r = ro = yp = qp = sp = None
+    q_type = QUANT_NONE
     if residual is not None:
-        r_type = _dense("residual", residual, shp, floats, None)
-        if residual_out is not None:
-            _dense("residual_out", residual_out, shp, floats, r_type)
-    elif residual_out is not None:
-        r_type = _dense("residual_out", residual_out, shp, floats, None)
-    w_type = _dense("weight", weight, shp[1:], floats, None)
+        r_type = _tag("residual", residual, shape, floats, dev)
+        r = residual.data_ptr()
+    if residual_out is not None:
+        t = _tag("residual_out", residual_out, shape, floats, dev)
+        if r is not None and t != r_type:
+            raise ValueError(f"residual_out has type {residual_out.dtype}, residual {residual.dtype}")
+        r_type = t
+        ro = residual_out.data_ptr()
+    w_type = _tag("weight", weight, shape[1:], floats, dev)
     if y is not None:
-        _dense("y", y, shp, floats, TYPE_BF16)
-    q_type = QUANT_NONE if q is None else _dense("q", q, shp, codes, None)
-    _f32("scale", scale, M)
-    _on_current_device(x, residual, weight, residual_out, y, q, scale)
-    _check(_lib.moe_add_rmsnorm(M, H, _p(x), x_type, _p(residual), r_type, _p(weight), w_type, eps, _p(residual_out),
-                                _p(y), _p(q), q_type, _p(scale), _stream(stream)),
+        _tag("y", y, shape, bf16, dev)
+        yp = y.data_ptr()
+    if q is not None:
+        q_type = _tag("q", q, shape, codes, dev)
+        qp = q.data_ptr()
+    if scale is not None:
+        _vector("scale", scale, M, f32, dev)
+        sp = scale.data_ptr()
+    st = _stream_on(dev, stream)
+    _check(_lib.moe_add_rmsnorm(M, H, x.data_ptr(), x_type, r, r_type, weight.data_ptr(), w_type, eps, ro, yp, qp,
+                                q_type, sp, st),
            "moe_add_rmsnorm")
 
 
@@ -398,16 +445,19 @@ def router(num_experts: int, topk: int, score: str = "sigmoid", groups: int = 1,
 
 def moe_route_scores(rp: MoeRouterParams, logits, bias, topk_ids, topk_w, stream=None):
     """topk_ids [M,K] int32 and topk_w [M,K] float32 of logits [M,E] float32; bias [E] float32 or None."""
+    f32 = _types()[3]
     M = logits.shape[0]
-    _f32("logits", logits, M * rp.num_experts)
-    _f32("bias", bias, rp.num_experts)
-    _f32("topk_w", topk_w, M * rp.topk)
-    if topk_ids.numel() != M * rp.topk or topk_ids.element_size() != 4 or topk_ids.is_floating_point() \
-            or not topk_ids.is_contiguous():
-        raise ValueError(f"topk_ids must be a contiguous int32 tensor of {M * rp.topk} elements")
-    _on_current_device(logits, bias, topk_ids, topk_w)
-    _check(_lib.moe_route_scores(ctypes.byref(rp), M, _p(logits), _p(bias), _p(topk_ids), _p(topk_w),
-                                 _stream(stream)),
+    dev = logits.get_device()
+    _vector("logits", logits, M * rp.num_experts, f32, dev)
+    if bias is not None:
+        _vector("bias", bias, rp.num_experts, f32, dev)
+        bias = bias.data_ptr()
+    n = M * rp.topk
+    _vector("topk_ids", topk_ids, n, _ints()[0], dev)
+    _vector("topk_w", topk_w, n, f32, dev)
+    st = _stream_on(dev, stream)
+    _check(_lib.moe_route_scores(ctypes.byref(rp), M, logits.data_ptr(), bias, topk_ids.data_ptr(), topk_w.data_ptr(),
+                                 st),
            "moe_route_scores")
 
 
@@ -429,27 +479,33 @@ def moe_decode_forward_scored(shp, rp, M, hidden, router_w, bias, w13, w13_scale
 
 def moe_int8_quantize(x_bf16, q, scale, stream=None):
     """x_bf16 [rows, cols] -> int8 codes q [rows, cols] and scale [rows]."""
-    floats, codes = _types()
-    rows, cols = x_bf16.shape
-    _dense("x_bf16", x_bf16, x_bf16.shape, floats, TYPE_BF16)
-    _dense("q", q, x_bf16.shape, codes, QUANT_INT8)
-    _f32("scale", scale, rows)
-    _on_current_device(x_bf16, q, scale)
-    _check(_lib.moe_int8_quantize(_p(x_bf16), rows, cols, _p(q), _p(scale), _stream(stream)), "moe_int8_quantize")
+    _, _, bf16, f32 = _types()
+    shape = x_bf16.shape
+    rows, cols = shape
+    dev = x_bf16.get_device()
+    _tag("x_bf16", x_bf16, shape, bf16, dev)
+    _tag("q", q, shape, _ints()[1], dev)
+    _vector("scale", scale, rows, f32, dev)
+    st = _stream_on(dev, stream)
+    _check(_lib.moe_int8_quantize(x_bf16.data_ptr(), rows, cols, q.data_ptr(), scale.data_ptr(), st),
+           "moe_int8_quantize")
 
 
 def moe_int8_linear(a, a_scale, w, w_scale, out, stream=None):
     """out [M,N] (float32 or bf16) = (a [M,K] int8 times w [N,K] int8 transposed) * a_scale [M] * w_scale [N]."""
-    floats, codes = _types()
+    floats, _, _, f32 = _types()
+    int8 = _ints()[1]
     M, K = a.shape
     N = w.shape[0]
-    _dense("a", a, (M, K), codes, QUANT_INT8)
-    _dense("w", w, (N, K), codes, QUANT_INT8)
-    out_type = _dense("out", out, (M, N), floats, None)
-    _f32("a_scale", a_scale, M)
-    _f32("w_scale", w_scale, N)
-    _on_current_device(a, a_scale, w, w_scale, out)
-    _check(_lib.moe_int8_linear(_p(a), _p(a_scale), _p(w), _p(w_scale), M, N, K, _p(out), out_type, _stream(stream)),
+    dev = a.get_device()
+    _vector("a", a, M * K, int8, dev)
+    _tag("w", w, (N, K), int8, dev)
+    out_type = _tag("out", out, (M, N), floats, dev)
+    _vector("a_scale", a_scale, M, f32, dev)
+    _vector("w_scale", w_scale, N, f32, dev)
+    st = _stream_on(dev, stream)
+    _check(_lib.moe_int8_linear(a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), M, N, K,
+                                out.data_ptr(), out_type, st),
            "moe_int8_linear")
 
 

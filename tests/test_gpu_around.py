@@ -34,7 +34,7 @@ def _router(moe, E, K):
     return moe.router(E, K, score="sigmoid", groups=8, group_topk=4, factor=2.5)
 
 
-@pytest.mark.parametrize("M", [1, 2, 4, 8, 9, 40])
+@pytest.mark.parametrize("M", [1, 2, 4, 8, 9, 17])
 @pytest.mark.parametrize("shared", [False, True])
 def test_scored_layer_is_its_parts(moe, ling, M, shared):
     """moe_decode_forward_scored gives the bits of the calls it stands for, and the oracle's layer."""
@@ -123,7 +123,7 @@ class Step:
         return {k: v.bits().copy() for k, v in self.o.items()}
 
 
-@pytest.mark.parametrize("M", [1, 4, 40])
+@pytest.mark.parametrize("M", [1, 4, 12])
 def test_a_step(moe, ling, M):
     """Each stage against its plain form on the bits the stage before it gave."""
     w, dw, _ = ling
