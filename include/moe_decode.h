@@ -441,9 +441,10 @@ moe_status moe_int8_quantize(const uint16_t* x_bf16, int32_t rows, int32_t cols,
 /* out[m, n] = (sum_k a[m,k] * w[n,k]) * a_scale[m] * w_scale[n]: the product
  * of int8 token rows a [M,K] with int8 output channels w [N,K], summed exactly
  * in 32-bit integers, scaled in fp32 and rounded once to out_type; out [M,N].
- * Any M, N > 0 and 1 <= K <= 131071 (beyond, a 32-bit sum of products could
- * overflow).  Codes may be any int8 value.  a, w and out are 16-byte
- * aligned. */
+ * M, N > 0 with at most 8 million tiles of 256 x 256 between them (one
+ * launch's limit) and 1 <= K <= 131071 (beyond, a 32-bit sum of products could
+ * overflow); MOE_ERR_UNSUPPORTED_SHAPE otherwise.  Codes may be any int8 value.  a, w and out are
+ * 16-byte aligned. */
 moe_status moe_int8_linear(const int8_t* a, const float* a_scale, const int8_t* w, const float* w_scale,
                            int32_t M, int32_t N, int32_t K, void* out, int32_t out_type, void* stream);
 

@@ -111,15 +111,18 @@ hipError_t launch_int8_linear(const Int8Args& a, hipStream_t s)
     } else {
         if (gemv_fits(a, 2 * 256)) return gemv_tokens<2, 16, 2>(a, s);
     }
+    hipError_t e = hipErrorInvalidConfiguration;
     switch (best_tile(a.M, a.N)) {
-        case 0: return tiles<256, 256, 2, 4, 64, 4, 2>(a, s);
-        case 1: return tiles<128, 128, 2, 2, 128, 2, 2>(a, s);
-        case 2: return tiles<128, 64, 2, 2, 128, 2, 3>(a, s);
-        case 3: return tiles<64, 128, 2, 2, 128, 3, 3>(a, s);
-        case 4: return tiles<64, 64, 2, 2, 128, 3, 3>(a, s);
-        case 5: return tiles<32, 64, 1, 4, 128, 4, 3>(a, s);
-        default: return tiles<32, 32, 1, 2, 128, 4, 2>(a, s);
+        case 0: break;
+        case 1: e = tiles<128, 128, 2, 2, 128, 2, 2>(a, s); break;
+        case 2: e = tiles<128, 64, 2, 2, 128, 2, 3>(a, s); break;
+        case 3: e = tiles<64, 128, 2, 2, 128, 3, 3>(a, s); break;
+        case 4: e = tiles<64, 64, 2, 2, 128, 3, 3>(a, s); break;
+        case 5: e = tiles<32, 64, 1, 4, 128, 4, 3>(a, s); break;
+        default: e = tiles<32, 32, 1, 2, 128, 4, 2>(a, s); break;
     }
+    // the largest tiles are also what is left when there are too many smaller ones
+    return e == hipErrorInvalidConfiguration ? tiles<256, 256, 2, 4, 64, 4, 2>(a, s) : e;
 }
 
 }  // namespace moe

@@ -844,7 +844,7 @@ moe_status moe_route_scores(const moe_router_params* router, int32_t M, const fl
     if (st != MOE_OK) return st;
     if (M <= 0) return fail(MOE_ERR_INVALID_ARG, "M (%d) must be positive", M);
     CHECK_PTR(logits); CHECK_PTR(topk_ids); CHECK_PTR(topk_w);
-    CHECK_ALIGN(logits); CHECK_ALIGN(bias); CHECK_ALIGN4(topk_ids); CHECK_ALIGN4(topk_w);
+    CHECK_ALIGN4(logits); CHECK_ALIGN4(bias); CHECK_ALIGN4(topk_ids); CHECK_ALIGN4(topk_w);
     const size_t pairs = (size_t)M * router->topk * 4;
     const Range in[] = {{logits, (size_t)M * router->num_experts * 4, "logits"},
                         {bias, (size_t)router->num_experts * 4, "bias"}};
@@ -881,7 +881,7 @@ moe_status moe_decode_forward_scored(const moe_shape* shape, const moe_router_pa
                     router->topk, shape->num_experts, shape->topk);
     CHECK_PTR(hidden); CHECK_PTR(router_w); CHECK_PTR(w13); CHECK_PTR(w13_scale);
     CHECK_PTR(w2); CHECK_PTR(w2_scale); CHECK_PTR(out);
-    CHECK_ALIGN(hidden); CHECK_ALIGN(router_w); CHECK_ALIGN(bias); CHECK_ALIGN(w13); CHECK_ALIGN(w2); CHECK_ALIGN(out);
+    CHECK_ALIGN(hidden); CHECK_ALIGN(router_w); CHECK_ALIGN4(bias); CHECK_ALIGN(w13); CHECK_ALIGN(w2); CHECK_ALIGN(out);
     if ((st = check_shared(shared)) != MOE_OK) return st;
     if ((st = check_ws(shape, M, ws, ws_bytes)) != MOE_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
@@ -936,6 +936,8 @@ moe_status moe_int8_linear(const int8_t* a, const float* a_scale, const int8_t* 
     moe::Int8Args g{reinterpret_cast<const uint8_t*>(a), reinterpret_cast<const uint8_t*>(w), a_scale, w_scale, out,
                     M, N, K, out_type, 1};
     hipError_t e = moe::launch_int8_linear(g, static_cast<hipStream_t>(stream));
+    if (e == hipErrorInvalidConfiguration)
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "a product of %d x %d has more tiles than one launch takes", M, N);
     return e == hipSuccess ? MOE_OK : hip_fail(e, "int8 product launch");
 }
 

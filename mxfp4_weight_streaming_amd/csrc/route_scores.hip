@@ -11,7 +11,7 @@ namespace moe {
 hipError_t launch_route_scores(const ScoreArgs& a, hipStream_t s)
 {
     // workgroups of 4 waves, one token a wave; about as many as the chip holds at
-    // once, each striding over the tokens with the next token's logits in flight
+    // once, each striding over the tokens
     const dim3 grid((unsigned)std::min<int64_t>((a.M + 3) / 4, 2048)), block(256);
     const bool softmax = a.score == kScoreSoftmax;
 #define MOE_ROUTE_SCORES(PER)                                                                             \

@@ -5,10 +5,10 @@
 //   group value = sum of the n largest available c of the group
 //   ids = the K largest c in the group_topk best groups; w = s[ids] / sum * factor
 //
-// The ids are compared for equality by whoever checks a router, and two
-// experts' scores may be neighbours in fp32, so the scores are evaluated in
-// fp64 and rounded once: any evaluation that accurate gives the same fp32
-// values and so the same ids.  From there on everything is exact comparison
+// Two experts' scores may be neighbours in fp32, and a choice between them
+// should not hang on how a kernel approximates: the scores are evaluated in fp64
+// and rounded once, and any evaluation that accurate gives the same fp32 values
+// and so the same ids.  From there on everything is exact comparison
 // of fp32 keys and fp32 additions of two operands.
 //
 // One wave a token, PER consecutive experts a lane (E <= 64 PER), so that a
@@ -32,8 +32,9 @@ namespace moe {
 // e^x for |x| <= 200, relative error below 2^-45: x = n ln2 + r, |r| <= ln2 / 2,
 // the Taylor sum of e^r to r^11 / 11! (the next term is below 2^-47), times 2^n.
 // The sum of 1.5 * 2^52 and x / ln2 rounds to a whole number in its low word.
-// The coefficients are kept in scalar registers: as literals each product would
-// first copy one into a vector register.
+// The coefficients are put into scalar registers where they are used: as
+// literals each would be copied into vector registers, ahead of the loop over
+// the tokens, and stay there.
 struct ExpCoefs {
     double c[10];
     __device__ __forceinline__ ExpCoefs()
@@ -75,8 +76,9 @@ __device__ __forceinline__ double rcp_f64(double d)
 }
 
 // fl32(sigmoid(x)); beyond +-200 that is 0 or 1 anyway, and NaN gives 0 or 1.
-__device__ __forceinline__ float sigmoid_exact(float x, const ExpCoefs& k)
+__device__ __forceinline__ float sigmoid_exact(float x)
 {
+    const ExpCoefs k;
     return (float)rcp_f64(1.0 + exp_f64(-(double)__builtin_amdgcn_fmed3f(x, -200.0f, 200.0f), k));
 }
 
@@ -88,29 +90,35 @@ __device__ __forceinline__ float sigmoid_near(float x)
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * __builtin_amdgcn_fmed3f(x, -80.0f, 80.0f)));
 }
 
-// How far a choice value made of sigmoid_near may be from the exact one:
-// 2^-20, and the two sums' roundings.  Twice that, for safety.
+// How far a choice value c made of sigmoid_near may be from the exact one:
+// 2^-20, and the roundings of the two sums, 2^-24 |c| each.  Twice that, for
+// safety.
 __device__ __forceinline__ float near_margin(float c) { return 0x1p-19f + 0x1p-22f * fabsf(c); }
 
-// The two largest of a set of values (b1 >= b2); -inf where there is none.
+// Choice values are handled as orderable keys: comparisons of unsigned numbers,
+// without the care that fp32 minima and maxima take of NaN.  0 is below every
+// key; kNoChoice is the key of -inf, an unavailable expert's.
+constexpr uint32_t kNoChoice = 0x007FFFFFu;
+
+// The two largest of a set of keys (b1 >= b2).
 struct Top2 {
-    float b1, b2;
-    __device__ __forceinline__ void take(float v)
+    uint32_t b1, b2;
+    __device__ __forceinline__ void take(uint32_t v)
     {
-        b2 = fmaxf(b2, fminf(b1, v));
-        b1 = fmaxf(b1, v);
+        b2 = max(b2, min(b1, v));
+        b1 = max(b1, v);
     }
     __device__ __forceinline__ void take(const Top2& o)
     {
-        b2 = fmaxf(fminf(b1, o.b1), fmaxf(b2, o.b2));
-        b1 = fmaxf(b1, o.b1);
+        b2 = max(min(b1, o.b1), max(b2, o.b2));
+        b1 = max(b1, o.b1);
     }
 };
 
 template <int CTRL>
 __device__ __forceinline__ void merge_dpp(Top2& t)
 {
-    const Top2 o = {dpp_f32<CTRL>(t.b1), dpp_f32<CTRL>(t.b2)};
+    const Top2 o = {dpp_u32<CTRL>(t.b1), dpp_u32<CTRL>(t.b2)};
     t.take(o);
 }
 
@@ -138,9 +146,9 @@ __device__ __forceinline__ Both lane_pair(uint32_t v)
 template <int MASK>
 __device__ __forceinline__ void merge_pair(Top2& t)
 {
-    const Both b1 = lane_pair<MASK>(__float_as_uint(t.b1)), b2 = lane_pair<MASK>(__float_as_uint(t.b2));
-    t = Top2{__uint_as_float(b1.a), __uint_as_float(b2.a)};
-    t.take(Top2{__uint_as_float(b1.b), __uint_as_float(b2.b)});
+    const Both b1 = lane_pair<MASK>(t.b1), b2 = lane_pair<MASK>(t.b2);
+    t = Top2{b1.a, b2.a};
+    t.take(Top2{b1.b, b2.b});
 }
 
 // Merge over aligned runs of `lanes` lanes, a power of two.
@@ -168,7 +176,7 @@ struct ScoreLds {
             Candidate cand[kWave];
             uint64_t key[kWave];
         };
-        float c[kMaxExperts];
+        uint32_t choice[kMaxExperts];
     };
 };
 
@@ -178,20 +186,22 @@ __device__ __forceinline__ void wave_lds_fence()
     __builtin_amdgcn_wave_barrier();
 }
 
-// 16,384 tokens over 512 experts, sigmoid, 4 of 8 groups: 29 us (1.2 TB/s of
-// logits); over 256, softmax: 17 us; one token 4.9 us in a graph.  Bound by the
-// issue of ~500 instructions a token and the chain of reductions between them,
-// not by the logits' bytes (7 us).  Every score in fp64 took 31 us and 871
-// instructions; the first kernel, with groups and choice through LDS, 57 us.
-// Bounding the registers for 4 waves a SIMD instead of 3 spills and gains
-// nothing.
+// 16,384 tokens over 512 experts, sigmoid, 4 of 8 groups: 24 us (1.4 TB/s of
+// logits); over 256, softmax: 15 us; one token 4.3 us in a graph.  Bound by the
+// issue of vector instructions (583 a token at 512 experts, 9 cycles in 10 with
+// one in issue), not by the logits' bytes (7 us).  Every score in fp64 took 871
+// instructions and 31 us; the first kernel, with groups and choice through LDS,
+// 57 us.  Holding the next token's logits in registers gained nothing: it cost
+// waves.
 template <int PER, bool SOFTMAX>
 __global__ __launch_bounds__(256) void route_scores_kernel(ScoreArgs a)
 {
     __shared__ __attribute__((aligned(16))) ScoreLds lds_all[4];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
     ScoreLds& lds = lds_all[wv];
-    const int E = a.E, K = a.K, G = a.G, each = E / G, e0 = lane * PER;
+    const int E = a.E, K = a.K, G = a.G, each = E / G;
+    int e0 = lane * PER;
+    const int group0 = e0 / each, left0 = each - (e0 - group0 * each);
     const float none = -__builtin_inff();
     typedef uint32_t vec_t __attribute__((ext_vector_type(PER), aligned(4)));
     auto load = [&](const float* p, float (&v)[PER]) {     // this lane's experts of one row
@@ -207,19 +217,18 @@ __global__ __launch_bounds__(256) void route_scores_kernel(ScoreArgs a)
             for (int i = 0; i < PER; ++i) v[i] = e0 + i < E ? p[e0 + i] : none;
         }
     };
-    float bias[PER] = {};
-    if (a.bias != nullptr) load(a.bias, bias);
-    const ExpCoefs k;
+    float bias[PER] = {};                                  // no bias: + 0 changes no score
+    if (a.bias != nullptr) {
+        load(a.bias, bias);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) bias[i] = fmaxf(bias[i], none);   // NaN as -inf
+    }
     const int64_t stride = (int64_t)gridDim.x * 4;
     int64_t m = (int64_t)blockIdx.x * 4 + wv;
-    if (m >= a.M) return;
-    float ahead[PER];                                      // the next token's logits
-    load(a.logits + (size_t)m * E, ahead);
     for (; m < a.M; m += stride) {
+        asm volatile("" : "+v"(e0));                       // or every e0 + i stays in a register over all tokens
         float x[PER];
-#pragma unroll
-        for (int i = 0; i < PER; ++i) x[i] = ahead[i];
-        if (m + stride < a.M) load(a.logits + (size_t)(m + stride) * E, ahead);
+        load(a.logits + (size_t)m * E, x);
         // softmax: the largest logit, and 1 / the sum of exponentials
         float top = none;
         double inv = 0.0;
@@ -231,100 +240,118 @@ __global__ __launch_bounds__(256) void route_scores_kernel(ScoreArgs a)
             }
             top = wave_max(top);
         }
-        auto part = [&](float logit) { return logit > none ? exp_f64(fmax((double)logit - (double)top, -200.0), k) : 0.0; };
-        auto score_exact = [&](float logit) {
-            return SOFTMAX ? (float)(part(logit) * inv) : sigmoid_exact(logit, k);
+        auto part = [&](float logit, const ExpCoefs& k) {
+            return logit > none ? exp_f64(fmax((double)logit - (double)top, -200.0), k) : 0.0;
         };
-        // the choice value; -inf where the logit or the value is -inf or NaN.
-        // It is never -0: a score is at least +0.
+        auto score_exact = [&](float logit) {
+            return SOFTMAX ? (float)(part(logit, ExpCoefs()) * inv) : sigmoid_exact(logit);
+        };
+        // the choice value's key; kNoChoice where the logit is -inf or NaN or
+        // the bias -inf.  The value is never -0: a score is at least +0.
         auto choice = [&](float logit, float score, float b) {
-            const float v = a.bias != nullptr ? score + b : score;
-            return logit > none ? fmaxf(v, none) : none;
+            const uint32_t u = __float_as_uint(score + b);
+            return logit > none ? u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u) : kNoChoice;
         };
         int rank = kWave, id = 0;
         float w = 0.0f;
         for (bool exact = SOFTMAX;; exact = true) {
-            float c[PER];
+            uint32_t key[PER];
             if constexpr (SOFTMAX) {
+                const ExpCoefs k;
                 double ex[PER], sum = 0.0;
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
-                    ex[i] = part(x[i]);
+                    ex[i] = part(x[i], k);
                     sum += ex[i];
                 }
                 sum = wave_sum_f64(sum);
                 inv = sum > 0.0 ? rcp_f64(sum) : 0.0;
 #pragma unroll
-                for (int i = 0; i < PER; ++i) c[i] = choice(x[i], (float)(ex[i] * inv), bias[i]);
+                for (int i = 0; i < PER; ++i) key[i] = choice(x[i], (float)(ex[i] * inv), bias[i]);
             } else if (exact) {
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
                     float l = x[i];
                     asm volatile("" : "+v"(l));            // else computed for every token, ahead of the branch
-                    c[i] = choice(l, sigmoid_exact(l, k), bias[i]);
+                    key[i] = choice(l, sigmoid_exact(l), bias[i]);
+                    __builtin_amdgcn_sched_barrier(0);     // one at a time: the path is rare, its registers are not
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < PER; ++i) c[i] = choice(x[i], sigmoid_near(x[i]), bias[i]);
+                for (int i = 0; i < PER; ++i) key[i] = choice(x[i], sigmoid_near(x[i]), bias[i]);
             }
-            // the groups that stay
-            bool stays[PER];
+            if (E < PER * kWave) {                         // experts past E: out of the running
 #pragma unroll
-            for (int i = 0; i < PER; ++i) stays[i] = e0 + i < E;
+                for (int i = 0; i < PER; ++i)
+                    if (e0 + i >= E) key[i] = 0;
+            }
+            uint32_t best = 0;                             // the lane's largest key in the groups that stay
+#pragma unroll
+            for (int i = 0; i < PER; ++i) best = max(best, key[i]);
+            bool lane_stays = true;
             if (G > a.group_topk) {
-                auto value = [&](const Top2& t) { return a.group_score == 2 && t.b2 > none ? t.b1 + t.b2 : t.b1; };
+                // a group's value, of its two largest keys
+                auto value = [&](const Top2& t) {
+                    const float v = f32_from_orderable(t.b1);
+                    return a.group_score == 2 && t.b2 > kNoChoice ? v + f32_from_orderable(t.b2) : v;
+                };
                 // rank of a group among all, whose keys stand in lanes 0, step, 2 step, ...
-                auto rank_of = [&](uint32_t key, int step, int mine) {
+                auto rank_of = [&](uint32_t group_key, int step, int mine) {
                     int r = 0;
                     for (int g = 0; g < G; ++g) {
-                        const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)key, g * step);
-                        r += (other > key || (other == key && g < mine)) ? 1 : 0;
+                        const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)group_key, g * step);
+                        r += (other > group_key || (other == group_key && g < mine)) ? 1 : 0;
                     }
                     return r;
                 };
-                // near values: whether the last group that stays and the first
-                // that goes are too close to tell (a value is a sum of two)
-                auto open = [&](float v, bool group, bool stay) {
-                    const float last = -wave_max(group && stay ? -v : none), first = wave_max(group && !stay ? v : none);
-                    return !(last - first > 4.0f * near_margin(fmaxf(fabsf(last), fabsf(first))));
+                // near values: whether any group that goes may, within the
+                // errors of its two summands, be worth as much as one that stays
+                auto open = [&](const Top2& t, bool group, bool stay) {
+                    const float v = value(t), c2 = t.b2 > kNoChoice ? f32_from_orderable(t.b2) : 0.0f;
+                    float e = 2.0f * near_margin(fabsf(f32_from_orderable(t.b1)) + fabsf(c2));
+                    if (!(e < 0x1p127f)) e = 0.0f;         // no available expert, or +inf: exact
+                    const float last = f32_from_orderable(wave_min_u32(group && stay ? f32_orderable(v - e) : 0xFFFFFFFFu));
+                    const float first = f32_from_orderable(wave_max_u32(group && !stay ? f32_orderable(v + e) : 0u));
+                    return !(last > first);
                 };
                 const int run = each / PER;
                 bool unclear = false;
                 if (each % PER == 0 && (run & (run - 1)) == 0) {
-                    Top2 t = {none, none};
+                    Top2 t = {kNoChoice, kNoChoice};
 #pragma unroll
-                    for (int i = 0; i < PER; ++i) t.take(c[i]);
+                    for (int i = 0; i < PER; ++i) t.take(key[i]);
                     merge_lanes(t, run);
-                    const float v = value(t);
-                    const bool stay = rank_of(f32_orderable(v), run, lane / run) < a.group_topk;
-                    if (!exact) unclear = open(v, e0 < E, stay);
-#pragma unroll
-                    for (int i = 0; i < PER; ++i) stays[i] = stays[i] && stay;
+                    const uint32_t group_key = f32_orderable(value(t));
+                    lane_stays = rank_of(group_key, run, lane / run) < a.group_topk;
+                    if (!exact) unclear = open(t, e0 < E, lane_stays);
+                    if (!lane_stays) best = 0;
                 } else {                                   // lane g: group g, from LDS
 #pragma unroll
                     for (int i = 0; i < PER; ++i)
-                        if (e0 + i < E) lds.c[e0 + i] = c[i];
+                        if (e0 + i < E) lds.choice[e0 + i] = key[i];
                     wave_lds_fence();
-                    Top2 t = {none, none};
+                    Top2 t = {kNoChoice, kNoChoice};
                     if (lane < G)
-                        for (int i = 0; i < each; ++i) t.take(lds.c[lane * each + i]);
-                    const float v = value(t);
-                    const bool stay = rank_of(f32_orderable(v), 1, lane) < a.group_topk;
-                    if (!exact) unclear = open(v, lane < G, stay);
+                        for (int i = 0; i < each; ++i) t.take(lds.choice[lane * each + i]);
+                    const uint32_t group_key = f32_orderable(value(t));
+                    const bool stay = rank_of(group_key, 1, lane) < a.group_topk;
+                    if (!exact) unclear = open(t, lane < G, stay);
                     const uint64_t kept = __ballot(lane < G && stay);
+                    best = 0;
+                    int group = group0, left = left0;      // expert e0 + i: its group, and experts to the next
+                    asm volatile("" : "+v"(group));        // kept in this branch
 #pragma unroll
-                    for (int i = 0; i < PER; ++i) stays[i] = stays[i] && ((kept >> (min(e0 + i, E - 1) / each)) & 1);
+                    for (int i = 0; i < PER; ++i) {
+                        if (!((kept >> min(group, kMaxGroups - 1)) & 1)) key[i] = 0;   // (past E: 0 already)
+                        best = max(best, key[i]);
+                        if (--left == 0) {
+                            left = each;
+                            ++group;
+                        }
+                    }
                     wave_lds_fence();                      // the candidates take the LDS
                 }
                 if (unclear) continue;
-            }
-            // keys: 0 for what is out of the running, below every other; an
-            // unavailable expert's is that of -inf
-            uint32_t key[PER], best = 0;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                key[i] = stays[i] ? f32_orderable(c[i]) : 0u;
-                best = max(best, key[i]);
             }
             // Threshold: the largest key of each of 8 sets of lanes (l mod 8,
             // so that every group has lanes in every set) are 8 different
@@ -339,10 +366,11 @@ __global__ __launch_bounds__(256) void route_scores_kernel(ScoreArgs a)
             best = min(best, dpp_u32<kDppXor2>(best));
             best = min(best, dpp_u32<kDppHalfMirror>(best));
             uint32_t thr = max((uint32_t)__builtin_amdgcn_readlane((int)best, 0), 1u);
-            if (!exact && thr > f32_orderable(none)) {
+            if (!exact && thr > kNoChoice && thr < 0xFF800000u) {   // finite
                 const float v = f32_from_orderable(thr);
                 thr = f32_orderable(v - 2.0f * near_margin(v));
             }
+            if (!lane_stays) thr = 0xFFFFFFFFu;            // above every key
             uint64_t hit[PER];
             int nc = 0;
 #pragma unroll
@@ -357,7 +385,7 @@ __global__ __launch_bounds__(256) void route_scores_kernel(ScoreArgs a)
                     uint64_t most = 0;
 #pragma unroll
                     for (int i = 0; i < PER; ++i)
-                        most = max_u64(most, ((uint64_t)key[i] << 32) | (uint32_t)(0xFFFF - (e0 + i)));
+                        if (lane_stays) most = max_u64(most, ((uint64_t)key[i] << 32) | (uint32_t)(0xFFFF - (e0 + i)));
                     most = wave_max_u64(most);
                     const int e = 0xFFFF - (int)(uint32_t)(most & 0xFFFFu);
                     float l = 0.0f, b = 0.0f;
@@ -378,7 +406,7 @@ __global__ __launch_bounds__(256) void route_scores_kernel(ScoreArgs a)
                 if (rank < K) {
                     id = me.expert;
                     w = score_exact(me.logit);
-                    if (!(choice(me.logit, w, me.bias) > none)) w = 0.0f;
+                    if (choice(me.logit, w, me.bias) <= kNoChoice) w = 0.0f;
                 }
                 break;
             }
@@ -394,22 +422,23 @@ __global__ __launch_bounds__(256) void route_scores_kernel(ScoreArgs a)
             }
             wave_lds_fence();
             const Candidate me = lds.cand[lane];           // (behind the last: not used)
-            const float score = score_exact(me.logit), value = choice(me.logit, score, me.bias);
-            const uint64_t mine = lane < nc ? ((uint64_t)f32_orderable(value) << 32) | (uint32_t)(0xFFFF - me.expert) : 0;
+            const float score = score_exact(me.logit);
+            const uint32_t value = choice(me.logit, score, me.bias);
+            const uint64_t mine = lane < nc ? ((uint64_t)value << 32) | (uint32_t)(0xFFFF - me.expert) : 0;
             lds.key[lane] = mine;
             wave_lds_fence();
             int above = 0;
-            for (int j = 0; j < nc; j += 16) {             // broadcast reads, 16 keys a round trip
-                ulonglong2 kk[8];
+            for (int j = 0; j < nc; j += 8) {              // broadcast reads, 8 keys a round trip
+                ulonglong2 kk[4];
 #pragma unroll
-                for (int q = 0; q < 8; ++q) kk[q] = *reinterpret_cast<const ulonglong2*>(lds.key + j + 2 * q);
+                for (int q = 0; q < 4; ++q) kk[q] = *reinterpret_cast<const ulonglong2*>(lds.key + j + 2 * q);
 #pragma unroll
-                for (int q = 0; q < 8; ++q) above += (kk[q].x > mine ? 1 : 0) + (kk[q].y > mine ? 1 : 0);
+                for (int q = 0; q < 4; ++q) above += (kk[q].x > mine ? 1 : 0) + (kk[q].y > mine ? 1 : 0);
             }
             if (lane < nc) {
                 rank = above;
                 id = me.expert;
-                w = rank < K && value > none ? score : 0.0f;
+                w = rank < K && value > kNoChoice ? score : 0.0f;
             }
             wave_lds_fence();                              // the next token takes the LDS
             break;

@@ -78,8 +78,8 @@ def test_route_scores_refusals(moe):
     assert L.moe_route_scores(r, 1, None, None, FAR, FAR2, None) == -1
     assert L.moe_route_scores(r, 1, A, None, None, FAR2, None) == -1
     assert L.moe_route_scores(r, 1, A, None, FAR, None, None) == -1
-    assert L.moe_route_scores(r, 1, A + 4, None, FAR, FAR2, None) == -3
-    assert L.moe_route_scores(r, 1, A, A + 8, FAR, FAR2, None) == -3
+    assert L.moe_route_scores(r, 1, A + 2, None, FAR, FAR2, None) == -3
+    assert L.moe_route_scores(r, 1, A, A + 9, FAR, FAR2, None) == -3
     assert L.moe_route_scores(r, 1, A, None, FAR + 2, FAR2, None) == -3
     assert L.moe_route_scores(r, 1, A, None, FAR, FAR2 + 1, None) == -3
     assert L.moe_route_scores(r, 2, A, None, A + 508, FAR2, None) == -1     # ids over the end of the logits
@@ -106,7 +106,7 @@ def test_router_logits_and_scored_layer_refusals(moe):
 
     assert call(M=0) == -1
     assert call(hidden=None) == -1
-    assert call(bias=A + 4) == -3
+    assert call(bias=A + 2) == -3
     assert call(out=None) == -1
     assert call(ws=None) == -4
     assert call(n=need - 1) == -4
@@ -138,6 +138,8 @@ def test_int8_refusals(moe):
         assert call(at, 0) == -1
         assert call(at, -3) == -1
     assert call(6, 131072) == -2
+    big = [1 << 44, FAR, 1 << 45, FAR2, 2 ** 31 - 1, 2 ** 31 - 1, 16, 1 << 50, 0, None]
+    assert L.moe_int8_linear(*big) == -2                                     # beyond one launch's threads
     assert call(8, 2) == -1
     for at in (0, 2, 7):
         assert call(at, good[at] + 8) == -3

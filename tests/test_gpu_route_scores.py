@@ -42,7 +42,7 @@ def _check(moe, logits, bias, K, **kw):
 CASES = [(1, 1, 1, 1), (2, 2, 1, 1), (8, 8, 1, 1), (16, 2, 1, 1), (60, 4, 4, 2), (63, 7, 9, 5), (64, 8, 64, 8),
          (64, 6, 8, 3), (65, 5, 5, 2), (96, 3, 16, 15), (100, 1, 4, 4), (128, 8, 8, 4), (160, 6, 8, 3), (255, 8, 5, 1),
          (256, 8, 1, 1), (256, 8, 8, 4), (257, 8, 1, 1), (320, 7, 16, 14), (384, 8, 2, 1), (511, 8, 7, 3),
-         (512, 8, 1, 1), (512, 8, 8, 4), (512, 8, 64, 1), (512, 8, 16, 8)]
+         (129, 6, 43, 20), (495, 8, 55, 7), (512, 8, 1, 1), (512, 8, 8, 4), (512, 8, 64, 1), (512, 8, 16, 8)]
 
 
 @pytest.mark.parametrize("E,K,G,keep", CASES)
@@ -107,6 +107,35 @@ def test_unavailable_experts(moe, score, E, G, keep):
         gi, gw = _check(moe, logits, b, 8, score=score, groups=G, group_topk=keep, factor=1.5)
         assert not gw[0].any() and not gw[1].any()
         assert all(len(set(r)) == 8 for r in gi.tolist())
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("forced", [3, 8, 40, 200])
+@pytest.mark.parametrize("G,keep", [(1, 1), (8, 4)])
+def test_forced_and_large_biases(moe, score, forced, G, keep):
+    """+inf biases force experts (the lowest indexes first where they are many); huge ones swallow the scores."""
+    rng = np.random.default_rng(14)
+    logits = rng.standard_normal((20, 256)).astype(np.float32)
+    bias = (0.1 * rng.standard_normal(256)).astype(np.float32)
+    at = rng.permutation(256)[:forced]
+    for v in (np.inf, 1e30, -1e30, 3e7):
+        b = bias.copy()
+        b[at] = v
+        _check(moe, logits, b, 8, score=score, groups=G, group_topk=keep)
+
+
+@pytest.mark.parametrize("size", [1.0, 30.0, 1000.0, 3e5])
+@pytest.mark.parametrize("E,G,keep", [(256, 8, 4), (512, 64, 9), (48, 24, 7)])
+def test_groups_of_opposite_biases(moe, size, E, G, keep):
+    """Two available experts a group whose large biases cancel in the group's value, to the last bits."""
+    rng = np.random.default_rng(15)
+    logits = np.full((200, E), NEG, np.float32)
+    bias = np.zeros(E, np.float32)
+    for g in range(G):
+        a, b = g * (E // G), g * (E // G) + 1
+        logits[:, [a, b]] = rng.standard_normal((200, 2)).astype(np.float32)
+        bias[a], bias[b] = size, -size
+    _check(moe, logits, bias, 4, score="sigmoid", groups=G, group_topk=keep)
 
 
 def test_near_values(moe):
