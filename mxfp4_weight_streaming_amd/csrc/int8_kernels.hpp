@@ -8,8 +8,10 @@
 namespace moe {
 
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));   // at any address
+// at any address
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
 
 __device__ __forceinline__ float int8_scaled(int32_t acc, float a_scale, float w_scale)
 {
@@ -402,7 +404,6 @@ __global__ __launch_bounds__(64 * WM * WN, EU) void int8_tile_kernel(Int8Args g)
     for (int j = 0; j < FN; ++j)
 #pragma unroll
         for (int r = 0; r < 4; ++r) ws[j][r] = g.w_scale[min(n0 + (wn * FN + j) * 16 + (lane >> 4) * 4 + r, g.N - 1)];
-    const bool wide = g.N % 4 == 0;                      // a row's groups of 4 channels are aligned
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         const int64_t m = m0 + (wm * FM + i) * 16 + row;
@@ -415,21 +416,22 @@ __global__ __launch_bounds__(64 * WM * WN, EU) void int8_tile_kernel(Int8Args g)
 #pragma unroll
             for (int r = 0; r < 4; ++r) o[r] = int8_scaled(acc[j][i][r], as[i], ws[j][r]);
             const size_t p = (size_t)m * g.N + n;
+            const bool all = n + 4 <= g.N;               // a row may start at any address
             if (g.out_type == kTypeF32) {
                 float* out = static_cast<float*>(g.out) + p;
-                if (wide) *reinterpret_cast<f32x4*>(out) = f32x4{o[0], o[1], o[2], o[3]};
+                if (all) *reinterpret_cast<f32x4_any*>(out) = f32x4_any{o[0], o[1], o[2], o[3]};
                 else
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
+                    for (int r = 0; r < 3; ++r)
                         if (n + r < g.N) out[r] = o[r];
             } else {
                 uint16_t* out = static_cast<uint16_t*>(g.out) + p;
-                if (wide)
-                    *reinterpret_cast<u32x2*>(out) = u32x2{f32_to_bf16_bits(o[0]) | f32_to_bf16_bits(o[1]) << 16,
-                                                          f32_to_bf16_bits(o[2]) | f32_to_bf16_bits(o[3]) << 16};
+                if (all)
+                    *reinterpret_cast<u32x2_any*>(out) = u32x2_any{f32_to_bf16_bits(o[0]) | f32_to_bf16_bits(o[1]) << 16,
+                                                                  f32_to_bf16_bits(o[2]) | f32_to_bf16_bits(o[3]) << 16};
                 else
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
+                    for (int r = 0; r < 3; ++r)
                         if (n + r < g.N) out[r] = (uint16_t)f32_to_bf16_bits(o[r]);
             }
         }
