@@ -330,9 +330,10 @@ def moe_lm_head_forward(x_bf16, q, scale, logits, stream=None):
 
 
 # ---- around the expert layer --------------------------------------------------
-# These calls take sizes and types from the tensors, so they check them: each
-# tensor dense, on the current device, of a type the call knows.  bf16 data may
-# also come as int16 / uint16 bits, E4M3 codes as uint8.
+# These calls check their tensors: each dense, on the current device, of a type
+# the call knows, and of the shape that goes with the others (or, where M and the
+# layer's shape are arguments, large enough).  bf16 data may also come as int16 /
+# uint16 bits, E4M3 codes as uint8.
 TYPE_BF16, TYPE_F32 = 0, 1
 QUANT_NONE, QUANT_E4M3, QUANT_INT8 = 0, 1, 2
 SCORES = {"softmax": 0, "sigmoid": 1}
@@ -461,19 +462,65 @@ def moe_route_scores(rp: MoeRouterParams, logits, bias, topk_ids, topk_w, stream
            "moe_route_scores")
 
 
+def _device_of(*tensors):
+    """The device of the first tensor among tensors, int addresses and None; None if there is none."""
+    for t in tensors:
+        if t is not None and not isinstance(t, int):
+            return t.get_device()
+    return None
+
+
+def _held(name, t, n, types, device):
+    """The address of a dense tensor of at least n elements of one of `types` (None: any type of one byte).  Its
+    shape is the caller's: M and the layer's sizes are arguments, and a buffer may hold more tokens than M.  An int
+    address is taken as it is, and None is left to the call."""
+    if t is None or isinstance(t, int):
+        return t
+    known = t.element_size() == 1 if types is None else t.dtype in types
+    if not known or t.numel() < n or not t.is_contiguous() or t.get_device() != device:
+        kind = "a one-byte type" if types is None else " or ".join(map(str, types))
+        raise ValueError(f"{name} must be a contiguous tensor of at least {n} elements of {kind} on the other tensors' "
+                         f"device; it has {t.numel()} of {t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
 def moe_router_logits(shp, M, hidden, router_w, logits, stream=None):
-    _check(_lib.moe_router_logits(ctypes.byref(shp), M, _p(hidden), _p(router_w), _p(logits), _stream(stream)),
-           "moe_router_logits")
+    """logits [M,E] float32 of hidden [M,H] and router_w [E,H], both bf16: the router's part of the layer alone."""
+    _, _, bf16, f32 = _types()
+    H, E = shp.hidden, shp.num_experts
+    dev = _device_of(hidden, router_w, logits)
+    hidden = _held("hidden", hidden, M * H, bf16, dev)
+    router_w = _held("router_w", router_w, E * H, bf16, dev)
+    logits = _held("logits", logits, M * E, f32, dev)
+    st = _stream(stream) if dev is None else _stream_on(dev, stream)
+    _check(_lib.moe_router_logits(ctypes.byref(shp), M, hidden, router_w, logits, st), "moe_router_logits")
 
 
 def moe_decode_forward_scored(shp, rp, M, hidden, router_w, bias, w13, w13_scale, w2, w2_scale, out, ws, shared=None,
                               stream=None):
-    """The layer with routing by scores (rp from router()); shared as in moe_decode_forward_shared."""
-    sh = _shared(shared)
-    _check(_lib.moe_decode_forward_scored(ctypes.byref(shp), ctypes.byref(rp), M, _p(hidden), _p(router_w), _p(bias),
-                                          _p(w13), _p(w13_scale), _p(w2), _p(w2_scale),
-                                          ctypes.byref(sh) if sh is not None else None, _p(out), _p(ws), _nbytes(ws),
-                                          _stream(stream)),
+    """The layer with routing by scores (rp from router()); bias [E] float32 or None; shared as in
+    moe_decode_forward_shared."""
+    _, _, bf16, f32 = _types()
+    H, I, E = shp.hidden, shp.inter, shp.num_experts
+    dev = _device_of(hidden, router_w, out, ws)
+    if bias is not None and not isinstance(bias, int):
+        _vector("bias", bias, E, f32, dev)
+    hidden = _held("hidden", hidden, M * H, bf16, dev)
+    router_w = _held("router_w", router_w, E * H, bf16, dev)
+    sizes = (("w13", I * H), ("w13_scale", 2 * I * (H // 32)), ("w2", H * I // 2), ("w2_scale", H * (I // 32)))
+    weights = [_held(name, t, E * n, None, dev) for t, (name, n) in zip((w13, w13_scale, w2, w2_scale), sizes)]
+    sh = None
+    if shared is not None:
+        if len(shared) == 4:
+            shared = [_held("shared " + name, t, n, None, dev) for t, (name, n) in zip(shared, sizes)]
+        sh = _shared(shared)
+    out = _held("out", out, M * H, f32, dev)
+    if not ws.is_contiguous() or ws.get_device() != dev:
+        raise ValueError("ws must be a contiguous tensor on the other tensors' device")
+    st = _stream(stream) if dev is None else _stream_on(dev, stream)
+    _check(_lib.moe_decode_forward_scored(ctypes.byref(shp), ctypes.byref(rp), M, hidden, router_w, _p(bias), *weights,
+                                          ctypes.byref(sh) if sh is not None else None, out, ws.data_ptr(), _nbytes(ws),
+                                          st),
            "moe_decode_forward_scored")
 
 
