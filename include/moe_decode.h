@@ -341,11 +341,14 @@ moe_status moe_lm_head_forward(const uint16_t* x_bf16, int32_t M, const uint8_t*
  * `hidden`: the residual's addition with the RMS norm and an 8-bit output,
  * routing by scores with a balance bias and groups, and an int8 matrix
  * product for the dense projections and for the LM head at any token count.
- * These calls take run-time sizes (nothing is compiled per shape), use no
- * workspace, and keep the library's rules: dense row-major device tensors,
- * every argument checked before anything is enqueued, nothing allocated or
- * synchronised, sums in fixed orders.  Outputs may not overlap inputs or each
- * other, except where a call says so (MOE_ERR_INVALID_ARG). */
+ * These calls take run-time sizes (nothing is compiled per shape) and no
+ * workspace, except moe_router_logits and moe_decode_forward_scored, which run
+ * the layer's kernels and take its shapes, the latter also its workspace.  All
+ * keep the library's rules: dense row-major device tensors, every argument
+ * checked before anything is enqueued, nothing allocated or synchronised, sums
+ * in fixed orders.  Outputs (and the part of a workspace that a call uses) may
+ * not overlap inputs or each other, except where a call says so
+ * (MOE_ERR_INVALID_ARG). */
 
 /* Types of a tensor given as `const void*` / `void*`. */
 typedef enum { MOE_TYPE_BF16 = 0, MOE_TYPE_F32 = 1 } moe_type;

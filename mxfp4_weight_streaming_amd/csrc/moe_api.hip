@@ -884,10 +884,27 @@ moe_status moe_decode_forward_scored(const moe_shape* shape, const moe_router_pa
     CHECK_ALIGN(hidden); CHECK_ALIGN(router_w); CHECK_ALIGN4(bias); CHECK_ALIGN(w13); CHECK_ALIGN(w2); CHECK_ALIGN(out);
     if ((st = check_shared(shared)) != MOE_OK) return st;
     if ((st = check_ws(shape, M, ws, ws_bytes)) != MOE_OK) return st;
+    const Carved c = carve(shape, M, ws);
+    const size_t H = shape->hidden, I = shape->inter, E = shape->num_experts;
+    const size_t one[4] = {I * H, 2 * I * (H / 32), H * I / 2, H * (I / 32)};   // an expert's w13, scales, w2, scales
+    const moe_shared_expert none{}, &se = shared != nullptr ? *shared : none;
+    const Range in[] = {{hidden, (size_t)M * H * 2, "hidden"},
+                        {router_w, E * H * 2, "router_w"},
+                        {bias, E * 4, "bias"},
+                        {w13, E * one[0], "w13"},
+                        {w13_scale, E * one[1], "w13_scale"},
+                        {w2, E * one[2], "w2"},
+                        {w2_scale, E * one[3], "w2_scale"},
+                        {se.w13, one[0], "the shared expert's w13"},
+                        {se.w13_scale, one[1], "the shared expert's w13_scale"},
+                        {se.w2, one[2], "the shared expert's w2"},
+                        {se.w2_scale, one[3], "the shared expert's w2_scale"}};
+    // (of the workspace, the part that the call uses)
+    const Range written[] = {{out, (size_t)M * H * 4, "out"}, {ws, c.L.total, "the workspace"}};
+    if ((st = check_apart(in, written)) != MOE_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
     // the expert stages leave these parts of the workspace alone when the
     // routing and the codes are given
-    const Carved c = carve(shape, M, ws);
     float* logits = c.at<float>(c.L.logits);
     int32_t* ids = c.at<int32_t>(c.L.ids);
     float* w = c.at<float>(c.L.w);
