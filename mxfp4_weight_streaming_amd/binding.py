@@ -390,6 +390,14 @@ def _vector(name, t, n, types, device):
                          f"other tensors' device; it has {t.numel()} of {t.dtype} on {t.device}")
 
 
+def _rows(name, t, M, n, types, device):
+    """The same for M rows of n elements: [M, n], or any shape whose elements follow one another in that order (a first
+    dimension of M, or all in one dimension).  A transposed tensor is not that."""
+    if t.dim() > 1 and t.shape[0] != M:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, {(M, n)} is needed")
+    _vector(name, t, M * n, types, device)
+
+
 def _stream_on(device, stream):
     """The stream's handle; the tensors' device must be torch's current one, where kernels are launched."""
     current, handle = _current or _torch_current()
@@ -453,9 +461,8 @@ def moe_route_scores(rp: MoeRouterParams, logits, bias, topk_ids, topk_w, stream
     if bias is not None:
         _vector("bias", bias, rp.num_experts, f32, dev)
         bias = bias.data_ptr()
-    n = M * rp.topk
-    _vector("topk_ids", topk_ids, n, _ints()[0], dev)
-    _vector("topk_w", topk_w, n, f32, dev)
+    _rows("topk_ids", topk_ids, M, rp.topk, _ints()[0], dev)
+    _rows("topk_w", topk_w, M, rp.topk, f32, dev)
     st = _stream_on(dev, stream)
     _check(_lib.moe_route_scores(ctypes.byref(rp), M, logits.data_ptr(), bias, topk_ids.data_ptr(), topk_w.data_ptr(),
                                  st),

@@ -77,3 +77,17 @@ def test_good_tensors_reach_the_device(moe):
         moe.moe_decode_forward_scored(moe.shape(H, I, E, K), moe.router(E, K), M, **more)
     with pytest.raises(ValueError, match="current device"):
         moe.moe_router_logits(moe.shape(H, I, E, K), M, more["hidden"], more["router_w"], torch.zeros(M * E))
+
+
+def test_route_scores_transposed_outputs(moe):
+    """ids and weights come in rows of a token: tensors of as many elements with the tokens elsewhere are refused."""
+    rp = moe.router(E, K)
+    lg, ids, tw = torch.zeros(M, E), torch.empty(M, K, dtype=torch.int32), torch.empty(M, K)
+    for bad in (dict(topk_ids=torch.empty(K, M, dtype=torch.int32)), dict(topk_w=torch.empty(K, M)),
+                dict(topk_ids=torch.empty(1, M, K, dtype=torch.int32)), dict(topk_w=torch.empty(1, M * K)),
+                dict(topk_ids=torch.tensor(0, dtype=torch.int32))):
+        with pytest.raises(ValueError, match="topk_"):
+            moe.moe_route_scores(rp, lg, None, **{**dict(topk_ids=ids, topk_w=tw), **bad})
+    for good in (dict(), dict(topk_ids=ids.view(-1)), dict(topk_w=tw.view(M, 1, K)), dict(topk_w=tw.view(-1))):
+        with pytest.raises(ValueError, match="current device"):
+            moe.moe_route_scores(rp, lg, None, **{**dict(topk_ids=ids, topk_w=tw), **good})
