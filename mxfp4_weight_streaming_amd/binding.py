@@ -399,11 +399,17 @@ def _rows(name, t, M, n, types, device):
 
 
 def _stream_on(device, stream):
-    """The stream's handle; the tensors' device must be torch's current one, where kernels are launched."""
+    """The stream's handle; the tensors' device must be torch's current one, where kernels are launched, and the
+    stream's."""
     current, handle = _current or _torch_current()
     if device != current():
         raise ValueError(f"the tensors are on device {device}, the current device is {current()}")
-    return handle(device) if stream is None else _stream(stream)
+    if stream is None:
+        return handle(device)
+    other = device if isinstance(stream, int) else getattr(stream, "device_index", device)
+    if other != device:
+        raise ValueError(f"the tensors are on device {device}, the stream on device {other}")
+    return _stream(stream)
 
 
 def moe_add_rmsnorm(x, residual, weight, eps, residual_out, y=None, q=None, scale=None, stream=None):

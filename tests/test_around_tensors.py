@@ -1,6 +1,8 @@
 """CPU-only checks of what the binding of the operators around the expert layer
-refuses about tensors, beyond tests/test_around_abi.py: said before any device
-is asked for."""
+refuses about tensors and streams, beyond tests/test_around_abi.py: said before
+any device is asked for."""
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -91,3 +93,16 @@ def test_route_scores_transposed_outputs(moe):
     for good in (dict(), dict(topk_ids=ids.view(-1)), dict(topk_w=tw.view(M, 1, K)), dict(topk_w=tw.view(-1))):
         with pytest.raises(ValueError, match="current device"):
             moe.moe_route_scores(rp, lg, None, **{**dict(topk_ids=ids, topk_w=tw), **good})
+
+
+def test_stream_of_another_device(moe, monkeypatch):
+    """A stream of another device would run the kernel there, on this device's memory."""
+    assert moe._stream_on(0, SimpleNamespace(device_index=0, cuda_stream=77)) == 77
+    assert moe._stream_on(0, 78) == 78 and moe._stream_on(0, None) == 0
+    with pytest.raises(ValueError, match="the stream on device 1"):
+        moe._stream_on(0, SimpleNamespace(device_index=1, cuda_stream=77))
+    # through a call: tensors on the (made up) current device, a stream of another
+    monkeypatch.setattr(moe, "_current", (lambda: -1, lambda d: 0))
+    with pytest.raises(ValueError, match="the stream on device 1"):
+        moe.moe_route_scores(moe.router(E, K), torch.zeros(M, E), None, torch.empty(M, K, dtype=torch.int32),
+                             torch.empty(M, K), stream=SimpleNamespace(device_index=1, cuda_stream=0))
