@@ -412,9 +412,12 @@ typedef struct {
  *   topk_w [M,K] = s of those experts (not c), 0 for unavailable ones, divided
  *   by their sum if renormalise (a sum of 0 leaves zeros), times factor.
  * So ids are always distinct and in [0, E), and a token with no available
- * expert has weights 0.  The scores are correctly rounded up to an fp64
- * evaluation's error, so the ids do not depend on how a kernel sums or
- * approximates. */
+ * expert has weights 0.  The fp64 evaluation of s is off by less than 2^-50 of
+ * s (sigmoid) or 2^-46 (softmax): s is the correctly rounded score, unless the
+ * exact one lies that near the middle between two fp32 numbers (at most one in
+ * 2^25, or in 2^21), where it may be either of the two, and the ids those that follow
+ * from it.  From s on, nothing is approximated and no order of sums matters
+ * before the weights'. */
 moe_status moe_route_scores(const moe_router_params* router, int32_t M, const float* logits,
                             const float* bias, int32_t* topk_ids, float* topk_w, void* stream);
 

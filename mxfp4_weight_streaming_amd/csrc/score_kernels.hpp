@@ -6,10 +6,14 @@
 //   ids = the K largest c in the group_topk best groups; w = s[ids] / sum * factor
 //
 // Two experts' scores may be neighbours in fp32, and a choice between them
-// should not hang on how a kernel approximates: the scores are evaluated in fp64
-// and rounded once, and any evaluation that accurate gives the same fp32 values
-// and so the same ids.  From there on everything is exact comparison
-// of fp32 keys and fp32 additions of two operands.
+// should not hang on how a kernel approximates: the scores are evaluated in fp64,
+// off by less than 2^-50 of a sigmoid or 2^-46 of a softmax score (its
+// exponentials 2^-51, the sum of up to 512 of them 14 roundings, and a logit's
+// distance from the largest, up to 104 where it counts, up to 2^-47), and
+// rounded once.  Two evaluations that accurate give the same fp32 value unless
+// the exact one lies that near the middle between two fp32 numbers: at most one
+// score in 2^25, or in 2^21.  From there on everything is exact comparison of fp32
+// keys and fp32 additions of two operands.
 //
 // One wave a token, PER consecutive experts a lane (E <= 64 PER), so that a
 // group is a run of lanes and its two largest are found in registers.
@@ -24,44 +28,43 @@
 #pragma once
 
 #include "around_common.hpp"
+#include "exp_coefs.hpp"
 #include "moe_types.hpp"
 #include "topk_wave.hpp"        // f32_orderable
 
 namespace moe {
 
-// e^x for |x| <= 200, relative error below 2^-45: x = n ln2 + r, |r| <= ln2 / 2,
-// the Taylor sum of e^r to r^11 / 11! (the next term is below 2^-47), times 2^n.
-// The sum of 1.5 * 2^52 and x / ln2 rounds to a whole number in its low word.
+// e^x for |x| <= 200, relative error below 2^-51: x = n ln2 + r, |r| <= ln2 / 2,
+// 1 + r + r^2 q(r) with the constants of exp_coefs.hpp, times 2^n.  What is
+// off: q by 2^-55, r by 2^-54 (the two roundings of x - n ln2; ln2 to one
+// double only would add 2^-47 at n = 288), the last two steps by 2^-54.5 and
+// 2^-53: less than 2^-51.9 in all, 2^-52.4 the most seen
+// (tests/exp_f64_check.cpp).  The sum of 1.5 * 2^52 and x / ln2 rounds to a
+// whole number in its low word.
 // The coefficients are put into scalar registers where they are used: as
 // literals each would be copied into vector registers, ahead of the loop over
 // the tokens, and stay there.
 struct ExpCoefs {
-    double c[10];
+    double c[kExpTerms], ln2_low;
     __device__ __forceinline__ ExpCoefs()
     {
-        c[0] = 1.0 / 39916800.0;
-        c[1] = 1.0 / 3628800.0;
-        c[2] = 1.0 / 362880.0;
-        c[3] = 1.0 / 40320.0;
-        c[4] = 1.0 / 5040.0;
-        c[5] = 1.0 / 720.0;
-        c[6] = 1.0 / 120.0;
-        c[7] = 1.0 / 24.0;
-        c[8] = 1.0 / 6.0;
-        c[9] = 0.5;
 #pragma unroll
-        for (int i = 0; i < 9; ++i) asm volatile("" : "+s"(c[i]));
+        for (int i = 0; i < kExpTerms; ++i) c[i] = kExpQ[i];
+        ln2_low = kExpLn2Low;
+#pragma unroll
+        for (int i = 0; i < kExpTerms - 1; ++i) asm volatile("" : "+s"(c[i]));   // (0.5 needs no register)
+        asm volatile("" : "+s"(ln2_low));
     }
 };
 
 __device__ __forceinline__ double exp_f64(double x, const ExpCoefs& k)
 {
-    const double t = __builtin_fma(x, 0x1.71547652b82fep+0, 0x1.8p+52);
+    const double t = __builtin_fma(x, kExpLog2E, 0x1.8p+52);
     const double n = t - 0x1.8p+52;
-    const double r = __builtin_fma(-n, 0x1.62e42fefa39efp-1, x);
+    const double r = __builtin_fma(-n, k.ln2_low, __builtin_fma(-n, kExpLn2, x));
     double p = k.c[0];
 #pragma unroll
-    for (int i = 1; i < 10; ++i) p = __builtin_fma(p, r, k.c[i]);
+    for (int i = 1; i < kExpTerms; ++i) p = __builtin_fma(p, r, k.c[i]);
     p = __builtin_fma(p, r, 1.0);
     p = __builtin_fma(p, r, 1.0);
     return __builtin_amdgcn_ldexp(p, (int)(uint32_t)__builtin_bit_cast(uint64_t, t));
