@@ -53,9 +53,6 @@ __device__ __forceinline__ u32x4 int8_load_part(const uint8_t* p, int n, const u
 // Products by v_dot4_i32_i8.  Bound by the codes' read from HBM: 157,184 x 2,560
 // at 1 token 60.2 us (6.7 TB/s), at 4 tokens 65-68 us.
 // ---------------------------------------------------------------------------
-constexpr int kInt8GemvTokens = 4;
-constexpr int kInt8GemvLds = 64 * 1024;
-
 // Sum over aligned groups of L lanes, in every lane of the group.
 template <int L>
 __device__ __forceinline__ int32_t group_sum_i32(int32_t v)

@@ -3,6 +3,7 @@
 
 #include <algorithm>
 
+#include "around_choice.hpp"
 #include "moe_internal.hpp"
 #include "norm_kernels.hpp"
 
@@ -32,37 +33,42 @@ hipError_t norm(const NormArgs& a, hipStream_t s)
     return hipGetLastError();
 }
 
-// Few rows are a chain of latencies: more threads a row shorten it.  Many rows
-// are bound by bytes: fewer threads waste fewer lanes and need no barrier
-// (1,000 elements: 301 rows 4.9 us with a wave a row, 4.3 with 256 threads;
-// 16,384 rows 33.3 against 36.4).
-bool few(int64_t rows) { return rows < 2048; }
+template <int L, int V>
+hipError_t quantise(const uint16_t* x, int64_t rows, int cols, uint8_t* q, float* scale, hipStream_t s)
+{
+    hipLaunchKernelGGL((int8_quantize_kernel<L, V>), row_grid<L>(rows), dim3(RowShape<L>::kThreads), 0, s, x, rows, cols,
+                       q, scale);
+    return hipGetLastError();
+}
 
 }  // namespace
 
 hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t s)
 {
-    const int vecs = (a.H + 7) / 8;
-    if (vecs <= 16) return norm<16, 1>(a, s);
-    if (vecs <= 32) return norm<16, 2>(a, s);
-    if (vecs <= 64) return norm<64, 1>(a, s);
-    if (vecs <= 128 && !few(a.M)) return norm<64, 2>(a, s);
-    if (vecs <= 256) return norm<256, 1>(a, s);
-    if (vecs <= 512) return norm<512, 1>(a, s);
-    if (vecs <= 1024) return norm<512, 2>(a, s);
-    if (vecs <= 2048) return norm<512, 4>(a, s);
-    return norm<512, 8>(a, s);
+    switch (norm_variant(a.M, a.H)) {
+        case kNorm16x1: return norm<16, 1>(a, s);
+        case kNorm16x2: return norm<16, 2>(a, s);
+        case kNorm64x1: return norm<64, 1>(a, s);
+        case kNorm64x2: return norm<64, 2>(a, s);
+        case kNorm256x1: return norm<256, 1>(a, s);
+        case kNorm512x1: return norm<512, 1>(a, s);
+        case kNorm512x2: return norm<512, 2>(a, s);
+        case kNorm512x4: return norm<512, 4>(a, s);
+        default: return norm<512, 8>(a, s);
+    }
 }
 
 hipError_t launch_int8_quantize(const uint16_t* x, int rows, int cols, uint8_t* q, float* scale, hipStream_t s)
 {
-    const int64_t vecs = ((int64_t)cols + 7) / 8, n = rows;
-    if (vecs <= 16) hipLaunchKernelGGL((int8_quantize_kernel<16, 1>), row_grid<16>(n), dim3(256), 0, s, x, n, cols, q, scale);
-    else if (vecs <= 64) hipLaunchKernelGGL((int8_quantize_kernel<64, 1>), row_grid<64>(n), dim3(256), 0, s, x, n, cols, q, scale);
-    else if (vecs <= 128 && !few(n)) hipLaunchKernelGGL((int8_quantize_kernel<64, 2>), row_grid<64>(n), dim3(256), 0, s, x, n, cols, q, scale);
-    else if (vecs <= 512) hipLaunchKernelGGL((int8_quantize_kernel<512, 1>), row_grid<512>(n), dim3(512), 0, s, x, n, cols, q, scale);
-    else if (vecs <= 2048) hipLaunchKernelGGL((int8_quantize_kernel<512, 4>), row_grid<512>(n), dim3(512), 0, s, x, n, cols, q, scale);
-    else hipLaunchKernelGGL(int8_quantize_long_kernel, row_grid<64>(n), dim3(256), 0, s, x, n, cols, q, scale);
+    switch (quant_variant(rows, cols)) {
+        case kQuant16x1: return quantise<16, 1>(x, rows, cols, q, scale, s);
+        case kQuant64x1: return quantise<64, 1>(x, rows, cols, q, scale, s);
+        case kQuant64x2: return quantise<64, 2>(x, rows, cols, q, scale, s);
+        case kQuant512x1: return quantise<512, 1>(x, rows, cols, q, scale, s);
+        case kQuant512x4: return quantise<512, 4>(x, rows, cols, q, scale, s);
+        default: break;
+    }
+    hipLaunchKernelGGL(int8_quantize_long_kernel, row_grid<64>(rows), dim3(256), 0, s, x, (int64_t)rows, cols, q, scale);
     return hipGetLastError();
 }
 
