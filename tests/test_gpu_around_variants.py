@@ -2,7 +2,8 @@
 choose it (tests/_around_variants.py), bit for bit: the int8 product against
 exact sums, the norm and the quantiser against their plain forms; routing of
 more tokens than the chip holds waves, token for token against the plain
-implementation; the largest tile in a graph.
+implementation; the largest tile in a graph; more rows than a launch has
+workgroups, and tensors beyond 2^31 elements.
 """
 import numpy as np
 import pytest
@@ -160,3 +161,71 @@ def test_routing_of_more_tokens_than_waves(moe, score, E, G, keep):
         first = np.zeros(len(kinds), np.int64)
         first[at[::-1]] = np.arange(M)[::-1]
         assert same_f32(gw, gw[first[at]])
+
+
+# ---- many rows: workgroups that take a second row, offsets beyond 32 bits ---------------
+def _repeats(t, ref):
+    """Whether the rows of t are those of ref over and over, bit for bit."""
+    n = ref.shape[0]
+    bits = {1: torch.uint8, 2: torch.int16, 4: torch.int32}[t.element_size()]
+    t, ref = t.view(bits), ref.view(bits)
+    whole = t.shape[0] // n * n
+    return bool((t[:whole].unflatten(0, (-1, n)) == ref).all()) and torch.equal(t[whole:], ref[: t.shape[0] - whole])
+
+
+@pytest.mark.parametrize("M,H,kept", [((1 << 20) + 1003, 2051, 512), ((1 << 20) + 1003, 1025, 256), ((1 << 24) + 77, 129, 16)])
+def test_norm_of_more_rows_than_workgroups(moe, M, H, kept):
+    """Rows that repeat give the bits of one set of them, wherever they stand."""
+    rng = np.random.default_rng(H)
+    x = synth.bf16_from_f32((rng.standard_normal((kept, H)) * np.exp(rng.standard_normal((kept, 1)))).astype(np.float32))
+    w = synth.bf16_from_f32((1 + 0.2 * rng.standard_normal(H)).astype(np.float32))
+    _, yb, _ = rmsnorm(x, None, w, 1e-6, True)
+    rq, rs = int8_rows(yb)
+    dx = up(x).repeat(-(-M // kept), 1)[:M].contiguous()
+    y, q, s = Out((M, H), BF), Out((M, H), I8), Out((M,), F32)
+    moe.moe_add_rmsnorm(dx, None, up(w), 1e-6, None, y=y.t, q=q.t, scale=s.t)
+    torch.cuda.synchronize()
+    for o, ref in ((y, up(yb)), (q, up(rq)), (s, up(rs))):
+        assert bool((o.raw[o.n:] == 0xA5).all()) and _repeats(o.t, ref)
+    # and the quantiser alone, on the norm's rows
+    q.t.zero_(), s.t.zero_()
+    moe.moe_int8_quantize(y.t, q.t, s.t)
+    torch.cuda.synchronize()
+    for o, ref in ((q, up(rq)), (s, up(rs))):
+        assert bool((o.raw[o.n:] == 0xA5).all()) and _repeats(o.t, ref)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_routing_offsets_beyond_32_bits(moe, score):
+    rng = np.random.default_rng(18)
+    E, K, M, kept = 512, 8, (1 << 22) + 300_001, 400
+    logits = rng.standard_normal((kept, E)).astype(np.float32)
+    opts = dict(score=score, groups=8, group_topk=4, factor=2.5)
+    ri, rw = route(logits, None, K, **opts)
+    dl = up(logits).repeat(-(-M // kept), 1)[:M].contiguous()
+    ids, w = Out((M, K), torch.int32), Out((M, K), F32)
+    moe.moe_route_scores(moe.router(E, K, **opts), dl, None, ids.t, w.t)
+    torch.cuda.synchronize()
+    assert bool((ids.raw[ids.n:] == 0xA5).all()) and bool((w.raw[w.n:] == 0xA5).all())
+    assert _repeats(ids.t, up(ri)) and _repeats(w.t, w.t[:kept].clone())
+    assert np.all(np.abs(w.t[:kept].cpu().numpy() - rw) <= 6.6e-7 * np.abs(rw) + 1e-44)
+
+
+@pytest.mark.parametrize("M,N,K", [(70001, 40, 65536), (70001, 40, 65537), (1, 70001, 65536), (3, 70001, 65537),
+                                   (9, 70001, 65552)])
+def test_int8_inputs_beyond_32_bits(moe, M, N, K):
+    """Codes of more than 2^32 bytes: sampled rows, the first and last among them."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(19)
+    a = torch.randint(-128, 128, (M, K), generator=g, device="cuda", dtype=I8)
+    w = torch.randint(-128, 128, (N, K), generator=g, device="cuda", dtype=I8)
+    sa, sw = 0.5 + torch.rand(M, generator=g, device="cuda"), 0.5 + torch.rand(N, generator=g, device="cuda")
+    out = Out((M, N), F32)
+    moe.moe_int8_linear(a, sa, w, sw, out.t)
+    torch.cuda.synchronize()
+    assert bool((out.raw[out.n:] == 0xA5).all())
+    for m in {0, M // 2, max(0, M - 300)}:
+        for n in {0, N // 2, max(0, N - 300)}:
+            rows, cols = slice(m, m + 300), slice(n, n + 300)
+            ref = ((a[rows].double() @ w[cols].double().t()).float() * sa[rows, None]) * sw[None, cols]
+            assert torch.equal(out.t[rows, cols].contiguous().view(torch.int32), ref.view(torch.int32))
