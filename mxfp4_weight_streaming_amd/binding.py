@@ -393,6 +393,8 @@ def _vector(name, t, n, types, device):
 def _rows(name, t, M, n, types, device):
     """The same for M rows of n elements: [M, n], or any shape whose elements follow one another in that order (a first
     dimension of M, or all in one dimension).  A transposed tensor is not that."""
+    if t.dtype in types and t.shape == (M, n) and t.is_contiguous() and t.get_device() == device:
+        return
     if t.dim() > 1 and t.shape[0] != M:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, {(M, n)} is needed")
     _vector(name, t, M * n, types, device)
