@@ -477,38 +477,38 @@ def moe_route_scores(rp: MoeRouterParams, logits, bias, topk_ids, topk_w, stream
            "moe_route_scores")
 
 
-def _device_of(*tensors):
-    """The device of the first tensor among tensors, int addresses and None; None if there is none."""
-    for t in tensors:
-        if t is not None and not isinstance(t, int):
-            return t.get_device()
-    return None
-
-
 def _held(name, t, n, types, device):
-    """The address of a dense tensor of at least n elements of one of `types` (None: any type of one byte).  Its
+    """The address of a dense tensor of at least n elements of one of `types` on a device (any, where it is None).  Its
     shape is the caller's: M and the layer's sizes are arguments, and a buffer may hold more tokens than M.  An int
     address is taken as it is, and None is left to the call."""
-    if t is None or isinstance(t, int):
+    if t is None or t.__class__ is int:
         return t
-    known = t.element_size() == 1 if types is None else t.dtype in types
-    if not known or t.numel() < n or not t.is_contiguous() or t.get_device() != device:
-        kind = "a one-byte type" if types is None else " or ".join(map(str, types))
-        raise ValueError(f"{name} must be a contiguous tensor of at least {n} elements of {kind} on the other tensors' "
-                         f"device; it has {t.numel()} of {t.dtype} on {t.device}")
-    return t.data_ptr()
+    if t.dtype in types and t.numel() >= n and t.is_contiguous() and (device is None or t.get_device() == device):
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous tensor of at least {n} elements of {' or '.join(map(str, types))} on "
+                     f"the other tensors' device; it has {t.numel()} of {t.dtype} on {t.device}")
+
+
+def _codes(name, t, n, device):
+    """The same for n bytes of codes or block scales, of any type of one byte."""
+    if t is None or t.__class__ is int:
+        return t
+    if t.nbytes == t.numel() >= n and t.is_contiguous() and (device is None or t.get_device() == device):
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous tensor of at least {n} one-byte elements on the other tensors' device; "
+                     f"it has {t.numel()} of {t.dtype} on {t.device}")
 
 
 def moe_router_logits(shp, M, hidden, router_w, logits, stream=None):
     """logits [M,E] float32 of hidden [M,H] and router_w [E,H], both bf16: the router's part of the layer alone."""
     _, _, bf16, f32 = _types()
     H, E = shp.hidden, shp.num_experts
-    dev = _device_of(hidden, router_w, logits)
-    hidden = _held("hidden", hidden, M * H, bf16, dev)
-    router_w = _held("router_w", router_w, E * H, bf16, dev)
-    logits = _held("logits", logits, M * E, f32, dev)
+    dev = next((t.get_device() for t in (logits, hidden, router_w) if t is not None and t.__class__ is not int), None)
+    x = _held("hidden", hidden, M * H, bf16, dev)
+    wr = _held("router_w", router_w, E * H, bf16, dev)
+    lg = _held("logits", logits, M * E, f32, dev)
     st = _stream(stream) if dev is None else _stream_on(dev, stream)
-    _check(_lib.moe_router_logits(ctypes.byref(shp), M, hidden, router_w, logits, st), "moe_router_logits")
+    _check(_lib.moe_router_logits(ctypes.byref(shp), M, x, wr, lg, st), "moe_router_logits")
 
 
 def moe_decode_forward_scored(shp, rp, M, hidden, router_w, bias, w13, w13_scale, w2, w2_scale, out, ws, shared=None,
@@ -517,25 +517,26 @@ def moe_decode_forward_scored(shp, rp, M, hidden, router_w, bias, w13, w13_scale
     moe_decode_forward_shared."""
     _, _, bf16, f32 = _types()
     H, I, E = shp.hidden, shp.inter, shp.num_experts
-    dev = _device_of(hidden, router_w, out, ws)
-    if bias is not None and not isinstance(bias, int):
+    dev = ws.get_device()                                # the device of a workspace, always a tensor
+    if not ws.is_contiguous():
+        raise ValueError("ws is not contiguous")
+    x = _held("hidden", hidden, M * H, bf16, dev)
+    wr = _held("router_w", router_w, E * H, bf16, dev)
+    if bias is not None and bias.__class__ is not int:
         _vector("bias", bias, E, f32, dev)
-    hidden = _held("hidden", hidden, M * H, bf16, dev)
-    router_w = _held("router_w", router_w, E * H, bf16, dev)
-    sizes = (("w13", I * H), ("w13_scale", 2 * I * (H // 32)), ("w2", H * I // 2), ("w2_scale", H * (I // 32)))
-    weights = [_held(name, t, E * n, None, dev) for t, (name, n) in zip((w13, w13_scale, w2, w2_scale), sizes)]
+        bias = bias.data_ptr()
+    n13, ns13, n2, ns2 = I * H, 2 * I * (H // 32), H * I // 2, H * (I // 32)
+    c13, s13 = _codes("w13", w13, E * n13, dev), _codes("w13_scale", w13_scale, E * ns13, dev)
+    c2, s2 = _codes("w2", w2, E * n2, dev), _codes("w2_scale", w2_scale, E * ns2, dev)
     sh = None
     if shared is not None:
+        sizes = (("w13", n13), ("w13_scale", ns13), ("w2", n2), ("w2_scale", ns2))
         if len(shared) == 4:
-            shared = [_held("shared " + name, t, n, None, dev) for t, (name, n) in zip(shared, sizes)]
-        sh = _shared(shared)
-    out = _held("out", out, M * H, f32, dev)
-    if not ws.is_contiguous() or ws.get_device() != dev:
-        raise ValueError("ws must be a contiguous tensor on the other tensors' device")
-    st = _stream(stream) if dev is None else _stream_on(dev, stream)
-    _check(_lib.moe_decode_forward_scored(ctypes.byref(shp), ctypes.byref(rp), M, hidden, router_w, _p(bias), *weights,
-                                          ctypes.byref(sh) if sh is not None else None, out, ws.data_ptr(), _nbytes(ws),
-                                          st),
+            shared = [_codes("shared " + name, t, n, dev) for t, (name, n) in zip(shared, sizes)]
+        sh = ctypes.byref(_shared(shared))
+    o = _held("out", out, M * H, f32, dev)
+    _check(_lib.moe_decode_forward_scored(ctypes.byref(shp), ctypes.byref(rp), M, x, wr, bias, c13, s13, c2, s2, sh, o,
+                                          ws.data_ptr(), ws.nbytes, _stream_on(dev, stream)),
            "moe_decode_forward_scored")
 
 
