@@ -73,8 +73,11 @@ constexpr TileShape kTileShapes[kTiles] = {{256, 256, 64, 4, 2.78}, {128, 128, 1
 // Large tiles move the fewest bytes a product, small ones fill the chip when
 // there are few: each shape's time is its cost times the tiles a compute unit
 // gets, between the mean and the most (the busiest unit overlaps its tiles).
-// Measured against the best of a sweep at 22 sizes from 8 x 1536 x 768 to
-// 512 x 157184 x 2560: within 10% of it at each.
+// Measured against the best of the seven at 22 sizes from 8 x 1536 x 768 to
+// 512 x 157184 x 2560: within 6% of it at 17, and 17 to 19% above it at five
+// with 2.5 to 10 tiles of 64 x 64 a compute unit, where a size smaller than the
+// one chosen is faster (512 x 5120 x 2560: 18.7 us with 128 x 64, 15.8 with
+// 64 x 64).
 constexpr Int8Variant int8_tile(int64_t M, int64_t N)
 {
     int best = 0;

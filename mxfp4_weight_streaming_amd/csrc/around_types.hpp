@@ -11,7 +11,7 @@ enum : int { kTypeBf16 = 0, kTypeF32 = 1 };
 enum : int { kQuantNone = 0, kQuantE4m3 = 1, kQuantInt8 = 2 };
 enum : int { kScoreSoftmax = 0, kScoreSigmoid = 1 };
 
-constexpr int kMaxNormHidden = 32768;   // a row as fp32 fits a workgroup's LDS
+constexpr int kMaxNormHidden = 32768;   // 512 threads with 8 vectors of 8 elements each hold a row
 constexpr int kMaxGroups = 64;          // one lane a group
 constexpr int kMaxInt8Depth = 131071;   // 131071 * 128 * 128 < 2^31
 

@@ -180,12 +180,13 @@ __global__ __launch_bounds__(256) void int8_gemv_kernel(Int8Args g)
 // channels of one token: one 16-byte store in fp32.
 //
 // What bounds it, from stamps of the phases (256 x 256 tiles): at 4096 x 4096 x
-// 2560, one tile a compute unit, 46-50 us of which 1.8 us until the first step
-// has landed, 37 us in the steps (20.7 us of them the matrix cores' own time at
+// 2560, one tile a compute unit, 46-50 us of which 2.6 us until the first step
+// has landed, 36 us in the steps (20.7 us of them the matrix cores' own time at
 // the ~2.1 GHz they run at; reads from LDS take nearly as long and overlap
-// partly) and 8 us in the stores.  At 10240 codes of K the same product runs at
-// 2.3 POP/s.  Small products are a chain of latencies: 77 x 2560 x 768, 4.0 us,
-// has 0.9 us to the first step, 1.1 us of steps and 0.8 us of scales and stores.
+// partly) and 8 us in the scales and stores.  At 10240 codes of K the same
+// product runs at 2.1-2.3 POP/s.  Small products are a chain of latencies: 77 x
+// 2560 x 768, 4.0 us, has 1.0 us to the first step, 1.3 us of steps and 0.9 us
+// of scales and stores.
 // ---------------------------------------------------------------------------
 template <int BK>
 __device__ __forceinline__ int int8_swizzle(int r)

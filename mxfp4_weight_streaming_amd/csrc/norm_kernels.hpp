@@ -92,7 +92,8 @@ __device__ __forceinline__ void store8(void* p, size_t i, int n, const Raw8<F32>
 // L threads a row (a DPP row of 16 lanes, a wave, or a workgroup of L), V
 // vectors of 8 elements a thread: the whole row stays in registers between the
 // reductions and the output, so each input is read once and nothing is read
-// back.
+// back.  (Beyond 16,384 elements, V = 8, not all of it: 34 registers a thread go
+// to scratch memory where x and the residual are fp32, 2 where one of them is.)
 template <int L>
 struct RowParts {
     static constexpr int kWaves = L > kWave ? L / kWave : 1;
@@ -155,8 +156,8 @@ __device__ __forceinline__ void store_codes(uint8_t* q, size_t at, int n, u32x2 
 }
 
 // Bound by the rows' bytes once there are enough of them: 16,384 rows of 2,560
-// (fp32 x, bf16 residual, y, E4M3 codes) 86.6-88.8 us, 5.2-5.3 TB/s, where a
-// copy reaches 4.9 TB/s; one row 3.4 us in a graph, a launch and three memory
+// (fp32 x, bf16 residual, y, E4M3 codes) 86-92 us, 5.0-5.3 TB/s, where a
+// copy reaches 4.9 TB/s; one row 3.2 us in a graph, a launch and three memory
 // latencies.  (The first kernel, a workgroup of 256 with the row in LDS and
 // single elements a load, took 145 us.)
 template <int L, int V, bool XF32, bool RF32>

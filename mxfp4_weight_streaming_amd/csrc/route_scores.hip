@@ -10,8 +10,9 @@ namespace moe {
 
 hipError_t launch_route_scores(const ScoreArgs& a, hipStream_t s)
 {
-    // workgroups of 4 waves, one token a wave; about as many as the chip holds at
-    // once, each striding over the tokens
+    // workgroups of 4 waves, one token a wave, each striding over the tokens: as
+    // many as the chip holds at once at up to 128 experts or nearly (7 waves a
+    // SIMD: 1,792), and twice as many at 512 and sigmoid (4 waves: 1,024)
     const dim3 grid((unsigned)std::min<int64_t>((a.M + 3) / 4, 2048)), block(256);
     const bool softmax = a.score == kScoreSoftmax;
 #define MOE_ROUTE_SCORES(PER)                                                                             \

@@ -189,12 +189,12 @@ __device__ __forceinline__ void wave_lds_fence()
     __builtin_amdgcn_wave_barrier();
 }
 
-// 16,384 tokens over 512 experts, sigmoid, 4 of 8 groups: 24 us (1.4 TB/s of
-// logits); over 256, softmax: 15 us; one token 4.3 us in a graph.  Bound by the
-// issue of vector instructions (583 a token at 512 experts, 9 cycles in 10 with
-// one in issue), not by the logits' bytes (7 us).  Every score in fp64 took 871
-// instructions and 31 us; the first kernel, with groups and choice through LDS,
-// 57 us.  Holding the next token's logits in registers gained nothing: it cost
+// 16,384 tokens over 512 experts, sigmoid, 4 of 8 groups: 24-25 us (1.4 TB/s of
+// logits); over 256, softmax: 15 us; one token 4.4 us in a graph.  Bound by the
+// issue of vector instructions (613 a token at 512 experts, in issue 85% of the
+// time; 427 and 92% at 256, softmax), not by the logits' bytes (7 and 3 us).
+// Every score in fp64 took half as many again and 31 us; the first kernel, with
+// groups and choice through LDS, 57 us.  Holding the next token's logits in registers gained nothing: it cost
 // waves.
 template <int PER, bool SOFTMAX>
 __global__ __launch_bounds__(256) void route_scores_kernel(ScoreArgs a)
