@@ -454,6 +454,84 @@ moe_status moe_int8_quantize(const uint16_t* x_bf16, int32_t rows, int32_t cols,
 moe_status moe_int8_linear(const int8_t* a, const float* a_scale, const int8_t* w, const float* w_scale,
                            int32_t M, int32_t N, int32_t K, void* out, int32_t out_type, void* stream);
 
+/* ---- Beside the projections and the LM head -----------------------------------
+ * What a server answers with, and what it adds to a projection for some
+ * requests: log probabilities of given tokens, and low-rank adapters.  Run-time
+ * sizes; the library's rules as above.  The workspace is scratch: a call writes
+ * what it reads of it, so it needs no initialisation and may serve any other
+ * call, or a captured graph's, before or after; calls that overlap in time need
+ * one each. */
+
+/* Bytes of workspace that moe_token_logprobs needs for up to max_tokens rows of
+ * that vocabulary and topk (0: none); 0 for invalid sizes. */
+size_t moe_token_logprobs_workspace_bytes(int32_t max_tokens, int32_t vocab, int32_t topk);
+
+/* Log probabilities of one given token a row, with its rank, the row's entropy
+ * and its top alternatives.  logits [M, V] of logits_type, rows row_stride >= V
+ * elements apart (moe_lm_head_forward's, or moe_int8_linear's over the head; what
+ * lies between the rows is not read).  Of a row's logits l, with NaN counted as
+ * -inf and +inf as the largest finite fp32 value:
+ *   lse = log(sum_v exp(l_v)), the sum without its largest term held apart from
+ *       it, so that a confident row's lse keeps its digits;
+ *   logprob = l_t - lse of the token t = tokens[m]; -inf where l_t is -inf;
+ *   rank = how many v have l_v > l_t, or l_v = l_t and v < t (0: t is the best);
+ *   entropy = -sum_v p_v log p_v, p = exp(l - lse);
+ *   topk_ids, topk_logprob [M, topk]: the topk largest l_v above -inf in order
+ *       (ties: the lower index first) and their log probabilities; behind them,
+ *       where there are fewer, -1 and -inf.
+ * A row with nothing above -inf: logprob -inf, entropy 0.  A token below 0 asks
+ * for nothing: logprob 0, rank -1; one of V or more: -inf and V.
+ * With S = sum_v exp(l_v - max l), log S is off by at most 2^-17 of itself and
+ * the entropy by 2^-16 (the terms that carry the sums being within 25 of the
+ * largest logit), and each output by half a step of fp32 more; ids and ranks are
+ * exact.
+ * tokens [M] int32 goes with logprob and rank, of which one may be NULL; all
+ * three, entropy, and topk's two (with topk = 0) may be NULL, not everything.
+ * 0 <= topk <= 32; V <= row_stride <= 2^30.  logits is aligned to its elements
+ * (rows may start at any of them), ws to 256 bytes. */
+moe_status moe_token_logprobs(int32_t M, int32_t V, const void* logits, int32_t logits_type, int64_t row_stride,
+                              const int32_t* tokens, float* logprob, int32_t* rank, float* entropy, int32_t topk,
+                              int32_t* topk_ids, float* topk_logprob, void* ws, size_t ws_bytes, void* stream);
+
+/* Low-rank adapters of one projection, K = in_features to N = out_features, all
+ * of one rank r (pad smaller ones with zeros): num_adapters 1..65535, rank
+ * 1..128.  Device memory owned by the caller; a and b are 16-byte aligned. */
+typedef struct {
+    int32_t num_adapters;
+    int32_t rank;
+    int32_t in_features;
+    int32_t out_features;
+    const uint16_t* a;      /* [num_adapters, r, K] bf16 */
+    const uint16_t* b;      /* [num_adapters, N, r] bf16 */
+    const float* scale;     /* [num_adapters] fp32, or NULL (1) */
+} moe_lora;
+
+/* Bytes of workspace that moe_lora_add and moe_int8_linear_lora need for up to
+ * max_tokens tokens; 0 for invalid sizes. */
+size_t moe_lora_workspace_bytes(const moe_lora* lora, int32_t max_tokens);
+
+/* Adds each token's adapter to a projection's output.  For token m with adapter
+ * i = adapter_ids[m]:
+ *   u = scale[i] * (A[i] x[m])      products of bf16 values summed in fp32
+ *   out[m] = base[m] + B[i] u       u and the sums fp32, rounded once to out_type
+ * A token whose id is outside [0, num_adapters) has no adapter: out[m] = base[m].
+ * What a row becomes depends on its own token and adapter alone.
+ * x [M,K] bf16 (the projection's input), adapter_ids [M] int32 in any order,
+ * base [M,N] of out_type, or NULL (0); out [M,N], may be base itself.  x, base
+ * and out are 16-byte aligned. */
+moe_status moe_lora_add(const moe_lora* lora, int32_t M, const uint16_t* x, const int32_t* adapter_ids,
+                        const void* base, void* out, int32_t out_type, void* ws, size_t ws_bytes, void* stream);
+
+/* moe_int8_linear with adapters, in fp32 up to one rounding to out_type:
+ *   out[m] = (sum_k a[m,k] w[n,k]) * a_scale[m] * w_scale[n] + B[i] u
+ * a, a_scale, w, w_scale as in moe_int8_linear (K and N the adapters'); x [M,K]
+ * bf16, the same tokens before their quantisation (moe_add_rmsnorm gives both),
+ * which the adapters take.  Rows of tokens without an adapter are
+ * moe_int8_linear's, bit for bit. */
+moe_status moe_int8_linear_lora(const int8_t* a, const float* a_scale, const int8_t* w, const float* w_scale,
+                                const moe_lora* lora, int32_t M, const uint16_t* x, const int32_t* adapter_ids, void* out,
+                                int32_t out_type, void* ws, size_t ws_bytes, void* stream);
+
 /* Writes a one-line description of the kernels a call with this shape and M
  * would run (NUL-terminated, truncated to len).  Returns the same status the
  * call's shape validation would. */

@@ -61,6 +61,12 @@ class MoeRouterParams(ctypes.Structure):
                 ("renormalise", ctypes.c_int32), ("factor", ctypes.c_float)]
 
 
+class MoeLora(ctypes.Structure):
+    _fields_ = [("num_adapters", ctypes.c_int32), ("rank", ctypes.c_int32), ("in_features", ctypes.c_int32),
+                ("out_features", ctypes.c_int32), ("a", ctypes.c_void_p), ("b", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p)]
+
+
 class MoeJitReport(ctypes.Structure):
     _fields_ = [("from_cache", ctypes.c_int32), ("has_chunk_path", ctypes.c_int32), ("has_lm_head", ctypes.c_int32),
                 ("num_kernels", ctypes.c_int32), ("seconds", ctypes.c_double), ("cache_file", ctypes.c_char * 1024)]
@@ -77,6 +83,8 @@ _SH = ctypes.POINTER(MoeSharedExpert)
 _i32 = ctypes.c_int32
 _sz = ctypes.c_size_t
 _RP = ctypes.POINTER(MoeRouterParams)
+
+_LP = ctypes.POINTER(MoeLora)
 
 _SIGNATURES = {
     "moe_workspace_bytes": (_sz, [_S, _i32]),
@@ -105,6 +113,11 @@ _SIGNATURES = {
     "moe_decode_forward_scored": (ctypes.c_int, [_S, _RP, _i32, _V, _V, _V, _V, _V, _V, _V, _SH, _V, _V, _sz, _V]),
     "moe_int8_quantize": (ctypes.c_int, [_V, _i32, _i32, _V, _V, _V]),
     "moe_int8_linear": (ctypes.c_int, [_V, _V, _V, _V, _i32, _i32, _i32, _V, _i32, _V]),
+    "moe_token_logprobs_workspace_bytes": (_sz, [_i32, _i32, _i32]),
+    "moe_token_logprobs": (ctypes.c_int, [_i32, _i32, _V, _i32, ctypes.c_int64, _V, _V, _V, _V, _i32, _V, _V, _V, _sz, _V]),
+    "moe_lora_workspace_bytes": (_sz, [_LP, _i32]),
+    "moe_lora_add": (ctypes.c_int, [_LP, _i32, _V, _V, _V, _V, _i32, _V, _sz, _V]),
+    "moe_int8_linear_lora": (ctypes.c_int, [_V, _V, _V, _V, _LP, _i32, _V, _V, _V, _i32, _V, _sz, _V]),
     "moe_path_info": (ctypes.c_int, [_S, _i32, ctypes.c_char_p, _sz]),
     "moe_jit_build": (ctypes.c_int, [_S, ctypes.c_char_p, ctypes.c_char_p, ctypes.POINTER(MoeJitReport)]),
     "moe_jit_load": (ctypes.c_int, [_S, ctypes.c_char_p, _i32, ctypes.POINTER(MoeJitReport)]),
@@ -570,6 +583,142 @@ def moe_int8_linear(a, a_scale, w, w_scale, out, stream=None):
     _check(_lib.moe_int8_linear(a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), M, N, K,
                                 out.data_ptr(), out_type, st),
            "moe_int8_linear")
+
+
+# ---- beside the projections and the LM head -------------------------------------
+def _scratch(ws, device):
+    """Address and bytes of a workspace tensor, or of none."""
+    if ws is None:
+        return None, 0
+    if not ws.is_contiguous() or ws.get_device() != device:
+        raise ValueError(f"ws must be a contiguous tensor on the other tensors' device; it is on {ws.device}")
+    return ws.data_ptr(), ws.nbytes
+
+
+def logprobs_workspace(max_tokens: int, vocab: int, topk: int = 0, device="cuda"):
+    """A workspace (allocated through torch) for moe_token_logprobs of up to max_tokens rows."""
+    import torch
+    if max_tokens <= 0 or vocab <= 0 or topk < 0:
+        raise ValueError(f"max_tokens ({max_tokens}) and vocab ({vocab}) must be positive, topk ({topk}) not negative")
+    n = _lib.moe_token_logprobs_workspace_bytes(max_tokens, vocab, topk)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def moe_token_logprobs(logits, tokens=None, logprob=None, rank=None, entropy=None, topk_ids=None, topk_logprob=None,
+                       ws=None, stream=None):
+    """Log probabilities of the rows' given tokens, their ranks, the rows' entropies and their top alternatives.
+
+    logits [M,V] float32 or bf16, its rows any distance apart; tokens [M] int32 with logprob [M] float32 and rank [M]
+    int32, of which either may be None; entropy [M] float32 or None; topk_ids [M,k] int32 and topk_logprob [M,k]
+    float32, or None both; ws from logprobs_workspace."""
+    floats, _, _, f32 = _types()
+    i32 = _ints()[0]
+    M, V = logits.shape
+    dev = logits.get_device()
+    kind = floats.get(logits.dtype)
+    if kind is None or (V > 1 and logits.stride(1) != 1):
+        raise ValueError(f"logits must be rows of float32 or bf16 elements next to each other; it has type {logits.dtype} "
+                         f"and strides {logits.stride()}")
+    stride = logits.stride(0) if M > 1 else V
+    tp = lp = rp = ep = ip = kp = None
+    topk = 0
+    if tokens is not None:
+        _vector("tokens", tokens, M, i32, dev)
+        tp = tokens.data_ptr()
+    if logprob is not None:
+        _vector("logprob", logprob, M, f32, dev)
+        lp = logprob.data_ptr()
+    if rank is not None:
+        _vector("rank", rank, M, i32, dev)
+        rp = rank.data_ptr()
+    if entropy is not None:
+        _vector("entropy", entropy, M, f32, dev)
+        ep = entropy.data_ptr()
+    if topk_ids is not None:
+        topk = topk_ids.shape[-1]
+        _tag("topk_ids", topk_ids, (M, topk), i32, dev)
+        ip = topk_ids.data_ptr()
+    if topk_logprob is not None:
+        _tag("topk_logprob", topk_logprob, (M, topk), f32, dev)
+        kp = topk_logprob.data_ptr()
+    wp, wn = _scratch(ws, dev)
+    _check(_lib.moe_token_logprobs(M, V, logits.data_ptr(), kind, stride, tp, lp, rp, ep, topk, ip, kp, wp, wn,
+                                   _stream_on(dev, stream)),
+           "moe_token_logprobs")
+
+
+def lora(a, b, scale=None) -> MoeLora:
+    """Adapters for moe_lora_add and moe_int8_linear_lora: a [L,r,K] and b [L,N,r] bf16, scale [L] float32 or None.  Keeps
+    the tensors alive, and takes them as they are then: what is written into them later counts."""
+    _, _, bf16, f32 = _types()
+    if a.dim() != 3 or b.dim() != 3:
+        raise ValueError(f"a and b must be [L,r,K] and [L,N,r]; they have {a.dim()} and {b.dim()} dimensions")
+    L, r, K = a.shape
+    N = b.shape[1]
+    dev = a.get_device()
+    _tag("a", a, (L, r, K), bf16, dev)
+    _tag("b", b, (L, N, r), bf16, dev)
+    if scale is not None:
+        _vector("scale", scale, L, f32, dev)
+    lp = MoeLora(L, r, K, N, a.data_ptr(), b.data_ptr(), _p(scale))
+    lp.held = (a, b, scale)
+    lp.device = dev
+    return lp
+
+
+def moe_lora_workspace_bytes(lp: MoeLora, max_tokens: int) -> int:
+    return _lib.moe_lora_workspace_bytes(ctypes.byref(lp), max_tokens)
+
+
+def lora_workspace(lp: MoeLora, max_tokens: int):
+    """A workspace (allocated through torch) for up to max_tokens tokens."""
+    import torch
+    n = moe_lora_workspace_bytes(lp, max_tokens)
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_lora_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=lp.held[0].device)
+
+
+def moe_lora_add(lp: MoeLora, x, adapter_ids, base, out, ws, stream=None):
+    """out [M,N] = base + B[i] (scale[i] A[i] x) for the adapter i = adapter_ids[m] of each token, base where there is none.
+
+    x [M,K] bf16; adapter_ids [M] int32; base [M,N] float32 or bf16, as out, or None (0); out may be base; ws from
+    lora_workspace."""
+    floats, _, bf16, _ = _types()
+    M, N, dev = x.shape[0], lp.out_features, lp.device
+    _tag("x", x, (M, lp.in_features), bf16, dev)
+    _vector("adapter_ids", adapter_ids, M, _ints()[0], dev)
+    out_type = _tag("out", out, (M, N), floats, dev)
+    bp = None
+    if base is not None:
+        if _tag("base", base, (M, N), floats, dev) != out_type:
+            raise ValueError(f"base has type {base.dtype}, out {out.dtype}")
+        bp = base.data_ptr()
+    wp, wn = _scratch(ws, dev)
+    _check(_lib.moe_lora_add(ctypes.byref(lp), M, x.data_ptr(), adapter_ids.data_ptr(), bp, out.data_ptr(), out_type, wp,
+                             wn, _stream_on(dev, stream)),
+           "moe_lora_add")
+
+
+def moe_int8_linear_lora(a, a_scale, w, w_scale, lp: MoeLora, x, adapter_ids, out, ws, stream=None):
+    """moe_int8_linear with each token's adapter, rounded once: a [M,K] and w [N,K] int8 with their scales, x [M,K] bf16
+    the tokens that a was quantised from, adapter_ids [M] int32, out [M,N] float32 or bf16; ws from lora_workspace."""
+    floats, _, bf16, f32 = _types()
+    i32, int8 = _ints()
+    K, N, dev = lp.in_features, lp.out_features, lp.device
+    M = a.shape[0]
+    _tag("a", a, (M, K), int8, dev)
+    _tag("w", w, (N, K), int8, dev)
+    out_type = _tag("out", out, (M, N), floats, dev)
+    _vector("a_scale", a_scale, M, f32, dev)
+    _vector("w_scale", w_scale, N, f32, dev)
+    _tag("x", x, (M, K), bf16, dev)
+    _vector("adapter_ids", adapter_ids, M, i32, dev)
+    wp, wn = _scratch(ws, dev)
+    _check(_lib.moe_int8_linear_lora(a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), ctypes.byref(lp),
+                                     M, x.data_ptr(), adapter_ids.data_ptr(), out.data_ptr(), out_type, wp, wn,
+                                     _stream_on(dev, stream)),
+           "moe_int8_linear_lora")
 
 
 def _path_arg(p):

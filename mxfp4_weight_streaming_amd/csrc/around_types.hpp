@@ -13,6 +13,10 @@ enum : int { kScoreSoftmax = 0, kScoreSigmoid = 1 };
 
 constexpr int kMaxNormHidden = 32768;   // 512 threads with 8 vectors of 8 elements each hold a row
 constexpr int kMaxGroups = 64;          // one lane a group
+constexpr int kMaxAlternatives = 32;    // top alternatives of a row of logits
+constexpr int64_t kMaxRowStride = 1ll << 30;   // elements between rows of logits
+constexpr int kMaxLoraRank = 128;
+constexpr int kMaxAdapters = 65535;
 constexpr int kMaxInt8Depth = 131071;   // 131071 * 128 * 128 < 2^31
 
 struct NormArgs {
@@ -47,6 +51,32 @@ struct Int8Args {
     int64_t M, N;
     int K, out_type;
     int xm;                // tile kernels: parts along the tokens, of 8 (1, 2, 4 or 8)
+};
+
+struct LogprobArgs {
+    const void* logits;      // [M, V], rows `stride` elements apart
+    const int32_t* tokens;   // [M] or nullptr
+    float* logprob;          // [M] or nullptr
+    int32_t* rank;           // [M] or nullptr
+    float* entropy;          // [M] or nullptr
+    int32_t* topk_ids;       // [M, topk]
+    float* topk_logprob;
+    void* ws;
+    int64_t M, stride;
+    int V, type, topk;
+};
+
+struct LoraArgs {
+    const uint16_t* x;       // [M, K]
+    const uint16_t* a;       // [L, r, K]
+    const uint16_t* b;       // [L, N, r]
+    const float* scale;      // [L] or nullptr (1)
+    const int32_t* ids;      // [M]
+    const void* base;        // [M, N] or nullptr (0)
+    void* out;               // [M, N]
+    float* u;                // [M, r], workspace
+    int64_t M, N;
+    int K, r, L, base_type, out_type;
 };
 
 }  // namespace moe

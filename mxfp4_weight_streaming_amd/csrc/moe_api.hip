@@ -488,6 +488,41 @@ bool type_ok(int32_t t) { return t == MOE_TYPE_BF16 || t == MOE_TYPE_F32; }
 size_t type_bytes(int32_t t) { return t == MOE_TYPE_F32 ? 4 : 2; }
 bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
+// A workspace of the calls with run-time sizes; any (NULL too) where none is needed.
+moe_status check_scratch(const void* ws, size_t ws_bytes, size_t need, int32_t M)
+{
+    if (need == 0) return MOE_OK;
+    if (ws == nullptr) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
+    if (((uintptr_t)ws & 255u) != 0) return fail(MOE_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    if (ws_bytes < need)
+        return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed for M=%d", ws_bytes, need, M);
+    return MOE_OK;
+}
+
+moe_status check_lora(const moe_lora* l)
+{
+    if (l == nullptr) return fail(MOE_ERR_INVALID_ARG, "lora is NULL");
+    if (l->num_adapters <= 0 || l->rank <= 0 || l->in_features <= 0 || l->out_features <= 0)
+        return fail(MOE_ERR_INVALID_ARG, "adapters have a non-positive size (%d of rank %d, %d to %d features)",
+                    l->num_adapters, l->rank, l->in_features, l->out_features);
+    if (l->a == nullptr || l->b == nullptr) return fail(MOE_ERR_INVALID_ARG, "the adapters' a or b is NULL");
+    if (l->rank > moe::kMaxLoraRank)
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "rank (%d) above %d is not compiled", l->rank, moe::kMaxLoraRank);
+    if (l->num_adapters > moe::kMaxAdapters)
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%d adapters, above %d", l->num_adapters, moe::kMaxAdapters);
+    if (!aligned16(l->a) || !aligned16(l->b))
+        return fail(MOE_ERR_ALIGNMENT, "the adapters' a or b is not 16-byte aligned");
+    if (!aligned4(l->scale)) return fail(MOE_ERR_ALIGNMENT, "the adapters' scale is not 4-byte aligned");
+    return MOE_OK;
+}
+
+moe::LoraArgs lora_args(const moe_lora* l, int32_t M, const uint16_t* x, const int32_t* ids, const void* base, void* out,
+                        int32_t out_type, void* ws)
+{
+    return {x, l->a, l->b, l->scale, ids, base, out, static_cast<float*>(ws), M, l->out_features, l->in_features, l->rank,
+            l->num_adapters, out_type, out_type};
+}
+
 #define CHECK_ALIGN4(p)                                                                        \
     do {                                                                                       \
         if (!aligned4(p)) return fail(MOE_ERR_ALIGNMENT, "%s is not 4-byte aligned", #p);      \
@@ -956,6 +991,122 @@ moe_status moe_int8_linear(const int8_t* a, const float* a_scale, const int8_t* 
     if (e == hipErrorInvalidConfiguration)
         return fail(MOE_ERR_UNSUPPORTED_SHAPE, "a product of %d x %d has more tiles than one launch takes", M, N);
     return e == hipSuccess ? MOE_OK : hip_fail(e, "int8 product launch");
+}
+
+size_t moe_token_logprobs_workspace_bytes(int32_t max_tokens, int32_t vocab, int32_t topk)
+{
+    if (max_tokens <= 0 || vocab <= 0 || topk < 0 || topk > moe::kMaxAlternatives) return 0;
+    return moe::logprob_workspace(max_tokens, vocab, topk);
+}
+
+moe_status moe_token_logprobs(int32_t M, int32_t V, const void* logits, int32_t logits_type, int64_t row_stride,
+                              const int32_t* tokens, float* logprob, int32_t* rank, float* entropy, int32_t topk,
+                              int32_t* topk_ids, float* topk_logprob, void* ws, size_t ws_bytes, void* stream)
+{
+    CHECK_PTR(logits);
+    if (M <= 0 || V <= 0) return fail(MOE_ERR_INVALID_ARG, "M (%d) and V (%d) must be positive", M, V);
+    if (!type_ok(logits_type))
+        return fail(MOE_ERR_INVALID_ARG, "logits_type %d is neither bf16 (0) nor fp32 (1)", logits_type);
+    if (row_stride < V || row_stride > moe::kMaxRowStride)
+        return fail(MOE_ERR_INVALID_ARG, "row_stride (%lld) is not in V (%d)..2^30", (long long)row_stride, V);
+    if ((tokens != nullptr) != (logprob != nullptr || rank != nullptr))
+        return fail(MOE_ERR_INVALID_ARG, "tokens go together with logprob or rank, and are NULL without both");
+    if (topk < 0) return fail(MOE_ERR_INVALID_ARG, "topk (%d) is negative", topk);
+    if ((topk_ids != nullptr) != (topk > 0) || (topk_logprob != nullptr) != (topk > 0))
+        return fail(MOE_ERR_INVALID_ARG, "topk_ids and topk_logprob go together with a topk, and are NULL without one");
+    if (tokens == nullptr && entropy == nullptr && topk == 0) return fail(MOE_ERR_INVALID_ARG, "no output is asked for");
+    if (topk > moe::kMaxAlternatives)
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "topk (%d) above %d is not compiled", topk, moe::kMaxAlternatives);
+    if (((uintptr_t)logits & (type_bytes(logits_type) - 1)) != 0)
+        return fail(MOE_ERR_ALIGNMENT, "logits is not aligned to its elements");
+    CHECK_ALIGN4(tokens); CHECK_ALIGN4(logprob); CHECK_ALIGN4(rank); CHECK_ALIGN4(entropy);
+    CHECK_ALIGN4(topk_ids); CHECK_ALIGN4(topk_logprob);
+    moe_status st;
+    const size_t need = moe::logprob_workspace(M, V, topk), rows = (size_t)M * 4;
+    if ((st = check_scratch(ws, ws_bytes, need, M)) != MOE_OK) return st;
+    const Range in[] = {{logits, ((size_t)(M - 1) * row_stride + V) * type_bytes(logits_type), "logits"},
+                        {tokens, rows, "tokens"}};
+    const Range out[] = {{logprob, rows, "logprob"},
+                         {rank, rows, "rank"},
+                         {entropy, rows, "entropy"},
+                         {topk_ids, rows * topk, "topk_ids"},
+                         {topk_logprob, rows * topk, "topk_logprob"},
+                         {ws, need, "the workspace"}};
+    if ((st = check_apart(in, out)) != MOE_OK) return st;
+    moe::LogprobArgs a{logits, tokens, logprob, rank, entropy, topk_ids, topk_logprob, ws, M, row_stride, V, logits_type,
+                       topk};
+    hipError_t e = moe::launch_logprobs(a, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? MOE_OK : hip_fail(e, "log probability launch");
+}
+
+size_t moe_lora_workspace_bytes(const moe_lora* lora, int32_t max_tokens)
+{
+    if (check_lora(lora) != MOE_OK || max_tokens <= 0) return 0;
+    return moe::lora_workspace(max_tokens, lora->out_features, lora->rank);
+}
+
+moe_status moe_lora_add(const moe_lora* lora, int32_t M, const uint16_t* x, const int32_t* adapter_ids,
+                        const void* base, void* out, int32_t out_type, void* ws, size_t ws_bytes, void* stream)
+{
+    moe_status st = check_lora(lora);
+    if (st != MOE_OK) return st;
+    if (M <= 0) return fail(MOE_ERR_INVALID_ARG, "M (%d) must be positive", M);
+    CHECK_PTR(x); CHECK_PTR(adapter_ids); CHECK_PTR(out);
+    if (!type_ok(out_type)) return fail(MOE_ERR_INVALID_ARG, "out_type %d is neither bf16 (0) nor fp32 (1)", out_type);
+    CHECK_ALIGN(x); CHECK_ALIGN4(adapter_ids); CHECK_ALIGN(base); CHECK_ALIGN(out);
+    const size_t need = moe::lora_workspace(M, lora->out_features, lora->rank), L = lora->num_adapters, r = lora->rank,
+                 K = lora->in_features, N = lora->out_features, n = (size_t)M * N * type_bytes(out_type);
+    if ((st = check_scratch(ws, ws_bytes, need, M)) != MOE_OK) return st;
+    const Range in[] = {{x, (size_t)M * K * 2, "x"},
+                        {adapter_ids, (size_t)M * 4, "adapter_ids"},
+                        {base == out ? nullptr : base, n, "base"},
+                        {lora->a, L * r * K * 2, "the adapters' a"},
+                        {lora->b, L * N * r * 2, "the adapters' b"},
+                        {lora->scale, L * 4, "the adapters' scale"}};
+    const Range o[] = {{out, n, "out"}, {ws, need, "the workspace"}};
+    if ((st = check_apart(in, o)) != MOE_OK) return st;
+    if (overlap(o[1], {base, n, "base"})) return fail(MOE_ERR_INVALID_ARG, "the workspace overlaps base");
+    hipError_t e = moe::launch_lora_add(lora_args(lora, M, x, adapter_ids, base, out, out_type, ws),
+                                        static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? MOE_OK : hip_fail(e, "adapter launch");
+}
+
+moe_status moe_int8_linear_lora(const int8_t* a, const float* a_scale, const int8_t* w, const float* w_scale,
+                                const moe_lora* lora, int32_t M, const uint16_t* x, const int32_t* adapter_ids, void* out,
+                                int32_t out_type, void* ws, size_t ws_bytes, void* stream)
+{
+    moe_status st = check_lora(lora);
+    if (st != MOE_OK) return st;
+    CHECK_PTR(a); CHECK_PTR(a_scale); CHECK_PTR(w); CHECK_PTR(w_scale); CHECK_PTR(x); CHECK_PTR(adapter_ids);
+    CHECK_PTR(out);
+    if (M <= 0) return fail(MOE_ERR_INVALID_ARG, "M (%d) must be positive", M);
+    if (!type_ok(out_type)) return fail(MOE_ERR_INVALID_ARG, "out_type %d is neither bf16 (0) nor fp32 (1)", out_type);
+    if (lora->in_features > moe::kMaxInt8Depth)
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "K=%d above %d: a 32-bit sum could overflow", lora->in_features,
+                    moe::kMaxInt8Depth);
+    CHECK_ALIGN(a); CHECK_ALIGN(w); CHECK_ALIGN(x); CHECK_ALIGN(out);
+    CHECK_ALIGN4(a_scale); CHECK_ALIGN4(w_scale); CHECK_ALIGN4(adapter_ids);
+    const size_t need = moe::lora_workspace(M, lora->out_features, lora->rank), L = lora->num_adapters, r = lora->rank,
+                 K = lora->in_features, N = lora->out_features;
+    if ((st = check_scratch(ws, ws_bytes, need, M)) != MOE_OK) return st;
+    const Range in[] = {{a, (size_t)M * K, "a"},
+                        {w, N * K, "w"},
+                        {a_scale, (size_t)M * 4, "a_scale"},
+                        {w_scale, N * 4, "w_scale"},
+                        {x, (size_t)M * K * 2, "x"},
+                        {adapter_ids, (size_t)M * 4, "adapter_ids"},
+                        {lora->a, L * r * K * 2, "the adapters' a"},
+                        {lora->b, L * N * r * 2, "the adapters' b"},
+                        {lora->scale, L * 4, "the adapters' scale"}};
+    const Range o[] = {{out, (size_t)M * N * type_bytes(out_type), "out"}, {ws, need, "the workspace"}};
+    if ((st = check_apart(in, o)) != MOE_OK) return st;
+    moe::Int8Args p{reinterpret_cast<const uint8_t*>(a), reinterpret_cast<const uint8_t*>(w), a_scale, w_scale, out,
+                    M, (int64_t)N, (int)K, out_type, 1};
+    hipError_t e = moe::launch_int8_linear_lora(p, lora_args(lora, M, x, adapter_ids, nullptr, out, out_type, ws),
+                                                static_cast<hipStream_t>(stream));
+    if (e == hipErrorInvalidConfiguration)
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "a product of %d x %d has more tiles than one launch takes", M, (int)N);
+    return e == hipSuccess ? MOE_OK : hip_fail(e, "int8 product with adapters launch");
 }
 
 moe_status moe_path_info(const moe_shape* shape, int32_t M, char* buf, size_t len)
