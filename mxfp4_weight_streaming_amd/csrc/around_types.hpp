@@ -53,6 +53,10 @@ struct Int8Args {
     int xm;                // tile kernels: parts along the tokens, of 8 (1, 2, 4 or 8)
 };
 
+constexpr int kLogprobSegment = 4096;     // logits that four waves take at a time
+
+struct RowSums;
+
 struct LogprobArgs {
     const void* logits;      // [M, V], rows `stride` elements apart
     const int32_t* tokens;   // [M] or nullptr
@@ -64,6 +68,10 @@ struct LogprobArgs {
     void* ws;
     int64_t M, stride;
     int V, type, topk;
+    // by the launcher: LogprobPlan, and the workspace's parts
+    int segments, group_segments, groups, parts, part_segments;
+    float* maxima;           // [M][groups][256]
+    RowSums* sums;           // [M][parts]
 };
 
 struct LoraArgs {

@@ -2,18 +2,56 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
+#include "beside_choice.hpp"
 #include "logprob_kernels.hpp"
 #include "moe_internal.hpp"
 
 namespace moe {
 
-size_t logprob_workspace(int64_t, int, int) { return 0; }
+namespace {
+
+size_t maxima_bytes(int64_t M, const LogprobPlan& p) { return align256((size_t)M * p.groups * 256 * 4); }
+
+}  // namespace
+
+size_t logprob_workspace(int64_t M, int V, int topk)
+{
+    // what serves M rows serves fewer, so the most rows that are split count
+    const int64_t rows = std::min<int64_t>(M, kLogprobSplitRows);
+    const LogprobPlan p = logprob_plan(1, V);
+    if (p.parts == 1) return 0;
+    return (topk > 0 ? maxima_bytes(rows, p) : 0) + (size_t)rows * kLogprobMaxParts * sizeof(RowSums);
+}
+
+template <bool F32>
+static hipError_t launch(LogprobArgs a, hipStream_t s)
+{
+    const LogprobPlan p = logprob_plan(a.M, a.V);
+    a.segments = p.segments;
+    a.group_segments = p.group_segments;
+    a.groups = p.groups;
+    a.parts = p.parts;
+    a.part_segments = p.part_segments;
+    const dim3 rows((unsigned)std::min<int64_t>(a.M, 1 << 20)), block(256);
+    if (p.parts == 1) {
+        const size_t lds = a.topk > 0 ? (size_t)p.groups * 256 * 4 : 0;
+        hipLaunchKernelGGL((logprob_rows_kernel<F32>), rows, block, (uint32_t)lds, s, a);
+        return hipGetLastError();
+    }
+    a.maxima = static_cast<float*>(a.ws);
+    a.sums = reinterpret_cast<RowSums*>(static_cast<uint8_t*>(a.ws) + (a.topk > 0 ? maxima_bytes(a.M, p) : 0));
+    hipLaunchKernelGGL((logprob_parts_kernel<F32>), dim3((unsigned)(a.M * p.parts)), block, 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((logprob_join_kernel<F32>), rows, block, 0, s, a);
+    return hipGetLastError();
+}
 
 hipError_t launch_logprobs(const LogprobArgs& a, hipStream_t s)
 {
-    hipLaunchKernelGGL(logprob_row_kernel, dim3((unsigned)std::min<int64_t>(a.M, 1 << 20)), dim3(256), 0, s, a);
-    return hipGetLastError();
+    return a.type == kTypeF32 ? launch<true>(a, s) : launch<false>(a, s);
 }
 
 }  // namespace moe

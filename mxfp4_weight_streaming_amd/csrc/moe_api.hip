@@ -1033,8 +1033,20 @@ moe_status moe_token_logprobs(int32_t M, int32_t V, const void* logits, int32_t 
                          {topk_logprob, rows * topk, "topk_logprob"},
                          {ws, need, "the workspace"}};
     if ((st = check_apart(in, out)) != MOE_OK) return st;
-    moe::LogprobArgs a{logits, tokens, logprob, rank, entropy, topk_ids, topk_logprob, ws, M, row_stride, V, logits_type,
-                       topk};
+    moe::LogprobArgs a{};
+    a.logits = logits;
+    a.tokens = tokens;
+    a.logprob = logprob;
+    a.rank = rank;
+    a.entropy = entropy;
+    a.topk_ids = topk_ids;
+    a.topk_logprob = topk_logprob;
+    a.ws = ws;
+    a.M = M;
+    a.stride = row_stride;
+    a.V = V;
+    a.type = logits_type;
+    a.topk = topk;
     hipError_t e = moe::launch_logprobs(a, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? MOE_OK : hip_fail(e, "log probability launch");
 }
