@@ -53,8 +53,6 @@ struct Int8Args {
     int xm;                // tile kernels: parts along the tokens, of 8 (1, 2, 4 or 8)
 };
 
-constexpr int kLogprobSegment = 4096;     // logits that four waves take at a time
-
 struct RowSums;
 
 struct LogprobArgs {
@@ -70,7 +68,7 @@ struct LogprobArgs {
     int V, type, topk;
     // by the launcher: LogprobPlan, and the workspace's parts
     int segments, group_segments, groups, parts, part_segments;
-    float* maxima;           // [M][groups][256]
+    float* maxima;           // [M][groups][256 threads]
     RowSums* sums;           // [M][parts]
 };
 

@@ -12,24 +12,35 @@
 namespace moe {
 
 // ---- log probabilities -----------------------------------------------------------
-// A workgroup walks a row in segments of kLogprobSegment logits.  Few rows are
-// split into parts, a workgroup each, joined by a second kernel.
+// Each wave walks a row 1,024 logits at a time.  Rows of at most 1,024 have a
+// wave each; others a workgroup of 256, 512 or 1,024 threads, as many as give
+// every compute unit 16 waves; and where rows are too few for that, they are
+// split into parts of 256 threads, joined by a second kernel.
 constexpr int kLogprobMaxParts = 64;            // one lane each where they are joined
-constexpr int kLogprobMaxGroups = 40;           // of 256 threads: 40 KB of LDS
-constexpr int64_t kLogprobSplitRows = 512;      // fewer rows than this are split
+constexpr int kLogprobShort = 1024;
+constexpr int64_t kLogprobWaves = 16 * kCus;
+constexpr int64_t kLogprobSplitRows = 128;      // more rows than this are not split
 
 struct LogprobPlan {
-    int segments, group_segments, groups, parts, part_segments;
+    int threads, segments, group_segments, groups, parts, part_segments;   // threads 64: the short rows' kernel
 };
 
 constexpr LogprobPlan logprob_plan(int64_t M, int V)
 {
     LogprobPlan p{};
-    p.segments = (int)ceil_div(V, kLogprobSegment);
-    p.group_segments = (int)ceil_div(p.segments, kLogprobMaxGroups);
+    p.threads = 64;
+    p.parts = 1;
+    if (V <= kLogprobShort) return p;
+    const bool split = M <= kLogprobSplitRows && V > 16 * 1024;
+    p.threads = 256;
+    // (no more waves than there are segments for)
+    while (!split && p.threads < 1024 && M * p.threads / 64 < kLogprobWaves && V > 16 * p.threads) p.threads *= 2;
+    p.segments = (int)ceil_div(V, 16 * p.threads);
+    // the threads that read the groups' maxima hold 16 each: 1,024 of a row in
+    // parts, else those that wrote them
+    p.group_segments = (int)ceil_div(p.segments, split ? 64 : 16);
     p.groups = (int)ceil_div(p.segments, p.group_segments);
-    int64_t parts = M <= kLogprobSplitRows ? std::min<int64_t>(ceil_div(2048, M), kLogprobMaxParts) : 1;
-    parts = std::min<int64_t>(parts, p.groups);
+    const int64_t parts = split ? std::min<int64_t>({ceil_div(1024, M), kLogprobMaxParts, p.groups}) : 1;
     p.part_segments = (int)ceil_div(p.groups, parts) * p.group_segments;   // whole groups
     p.parts = (int)ceil_div(p.segments, p.part_segments);
     return p;

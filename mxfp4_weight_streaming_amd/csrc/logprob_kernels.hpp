@@ -29,11 +29,14 @@ namespace moe {
 
 constexpr int kLogprobGroupList = 256;      // groups read again
 constexpr int kLogprobCandidates = 512;     // logits ranked
+constexpr int kLogprobShortList = 128;      // ... of a row that one wave holds
+
+constexpr float kLargestLogit = 3.40282347e38f;
 
 // A logit's value as the definitions count it.
 __device__ __forceinline__ float logit_value(float x)
 {
-    return x != x ? -__builtin_inff() : __builtin_fminf(x, 3.40282347e38f) + 0.0f;   // (+ 0: no -0)
+    return __builtin_fminf(__builtin_fmaxf(__builtin_canonicalizef(x), -__builtin_inff()), kLargestLogit);
 }
 
 __device__ __forceinline__ float logit_at(const void* logits, bool f32, size_t i)
@@ -110,12 +113,35 @@ __device__ __forceinline__ int logit_place(int lane, int i)
     return (i / E) * (64 * E) + lane * E + i % E;
 }
 
+// The given token of a row, and its logit.
+struct Asked {
+    int token;                                           // (-1 where the call asks for none)
+    float mine;
+    bool inside;                                         // 0 <= token < V
+};
+
+template <bool F32>
+__device__ __forceinline__ Asked asked_of(const LogprobArgs& g, int64_t m, const uint8_t* row)
+{
+    Asked a;
+    a.token = g.tokens != nullptr ? g.tokens[m] : -1;
+    a.inside = a.token >= 0 && a.token < g.V;
+    a.mine = a.inside ? logit_at(row, F32, (size_t)a.token) : 0.0f;
+    return a;
+}
+
+template <bool F32>
+__device__ __forceinline__ const uint8_t* row_of(const LogprobArgs& g, int64_t m)
+{
+    return static_cast<const uint8_t*>(g.logits) + (size_t)m * (size_t)g.stride * (F32 ? 4 : 2);
+}
+
 // A wave's walk over its segments of one row's part.
 template <bool F32>
 struct LogitWalk {
     const uint8_t* row;
     int V, lane;
-    // given token
+    // the given token, if its rank is asked for
     int token;
     bool asked;
     float mine, above;                                   // its logit, and the next larger number
@@ -146,36 +172,30 @@ struct LogitWalk {
         }
     }
 
-    // Adds the 1,024 logits from `at`; returns the lane's largest.
+    // Adds the 1,024 logits from `at`; returns the lane's largest.  The logits
+    // stay as they are: the maxima pass over NaN, which the clamp of a distance
+    // takes to e^-256 = 0 as it does -inf; an infinite one is put right where
+    // it is met as the largest.
     __device__ __forceinline__ float add(int at, const Logits16<F32>& raw)
     {
         const float inf = __builtin_inff();
+        if (at >= V) return -inf;
         float x[16];
         float largest = -inf;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            x[i] = logit_value(raw.get(i));
+            x[i] = __builtin_canonicalizef(raw.get(i));  // (a signalling NaN would end a chain of v_max3)
             largest = fmaxf(largest, x[i]);
-        }
-        if (asked) {
-            if (at + 1024 <= V && (token >= at + 1024 || token < at)) {
-                // before the token equal logits count, behind it only larger ones
-                const float bar = token < at ? above : mine;
-                int below = 0;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) below += __popcll(__ballot(x[i] < bar));
-                ahead += 1024 - below;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int p = at + logit_place<F32>(lane, i);
-                    ahead += __popcll(__ballot(p < V && logit_before(x[i], p, mine, token)));
-                }
-            }
         }
         bool equal = false;                              // whether a logit may equal m
         if (__any(largest >= m)) {
-            const float most = wave_max(largest);
+            float most = wave_max(largest);
+            if (most == inf) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = x[i] == inf ? kLargestLogit : x[i];
+                largest = fminf(largest, kLargestLogit);
+                most = kLargestLogit;
+            }
             if (most > m) {
                 if (m > -inf) {
                     if (lane == 0) s += (double)top;
@@ -186,28 +206,46 @@ struct LogitWalk {
                 m = most;
                 top = 0;
             }
-            if (m == -inf) return largest;               // nothing yet
             equal = true;
         }
-        float ss[4] = {0.0f, 0.0f, 0.0f, 0.0f}, tt[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        auto sums = [&](auto exclude) {
+        if (m > -inf) {                                  // (else nothing yet)
+            float ss[4] = {0.0f, 0.0f, 0.0f, 0.0f}, tt[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            auto sums = [&](auto exclude) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                // (-256: e^y is 0 there and far above, and stays so for -inf)
-                const float y = fmaxf(x[i] - m, -256.0f);
-                float e = __builtin_amdgcn_exp2f(y * 1.44269504f);
-                if (exclude) {
-                    top += __popcll(__ballot(x[i] == m));
-                    e = x[i] == m ? 0.0f : e;
+                for (int i = 0; i < 16; ++i) {
+                    const float y = fmaxf(x[i] - m, -256.0f);
+                    float e = __builtin_amdgcn_exp2f(y * 1.44269504f);
+                    if constexpr (decltype(exclude)::value) {
+                        top += __popcll(__ballot(x[i] == m));
+                        e = x[i] == m ? 0.0f : e;
+                    }
+                    ss[i & 3] += e;
+                    tt[i & 3] = fmaf(e, y, tt[i & 3]);
                 }
-                ss[i & 3] += e;
-                tt[i & 3] = fmaf(e, y, tt[i & 3]);
+            };
+            if (equal) sums(std::true_type{});
+            else sums(std::false_type{});
+            s += (double)((ss[0] + ss[1]) + (ss[2] + ss[3]));
+            t += (double)((tt[0] + tt[1]) + (tt[2] + tt[3]));
+        }
+        if (asked) {
+            if (at + 1024 <= token && mine == -inf) {
+                ahead += 1024;                           // all are equal or larger
+            } else if (at + 1024 <= V && (at + 1024 <= token || token < at)) {
+                // before the token equal logits count, behind it only larger ones
+                const float bar = token < at ? above : mine;
+                int below = 0;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) below += __popcll(__ballot(!(x[i] >= bar)));
+                ahead += 1024 - below;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int p = at + logit_place<F32>(lane, i);
+                    ahead += __popcll(__ballot(p < V && logit_before(logit_value(x[i]), p, mine, token)));
+                }
             }
-        };
-        if (equal) sums(std::true_type{});
-        else sums(std::false_type{});
-        s += (double)((ss[0] + ss[1]) + (ss[2] + ss[3]));
-        t += (double)((tt[0] + tt[1]) + (tt[2] + tt[3]));
+        }
         return largest;
     }
 
@@ -217,92 +255,147 @@ struct LogitWalk {
     }
 };
 
+// Order of floats (no NaN) as unsigned numbers, and back.
+__device__ __forceinline__ uint32_t float_order(float x)
+{
+    const uint32_t u = __float_as_uint(x + 0.0f);        // (+ 0: no -0)
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+
+__device__ __forceinline__ float order_float(uint32_t o)
+{
+    return __uint_as_float(o ^ ((int32_t)o < 0 ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+template <int T>
 struct LogprobLds {
-    RowSums parts[4];
-    float columns[64 * 4];
-    float bests[64];
+    RowSums parts[T / kWave];
+    float columns[T];
+    uint32_t bests[64];
     int32_t groups[kLogprobGroupList];
-    float cand_x[kLogprobCandidates];
-    int32_t cand_i[kLogprobCandidates];
+    uint64_t cands[kLogprobCandidates];      // order of the logit, then the index backwards
+    double log_s;
+    float m;
     int32_t n_groups, n_cands;
+    float best_x[T];
+    int32_t best_i[T];
 };
 
-// A row's outputs, by a workgroup of 256 threads: from its sums, the largest
-// logit of each thread's groups (`best`) and of every group (`maxima`, group g
-// of thread i at g * 256 + i).
-template <bool F32>
-__device__ __forceinline__ void finish_row(const LogprobArgs& g, int64_t m, const RowSums& r, float best,
-                                           const float* maxima, LogprobLds& lds)
+__device__ __forceinline__ float log_p(float x, float m, double log_s)
 {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    return x == -__builtin_inff() ? x : (float)(((double)x - (double)m) - log_s);
+}
+
+// A row's outputs but the alternatives, by a wave that has its sums; returns log S.
+__device__ __forceinline__ double finish_sums(const LogprobArgs& g, int64_t m, const RowSums& r, const Asked& a)
+{
     const float inf = __builtin_inff();
-    const uint8_t* row = static_cast<const uint8_t*>(g.logits) + (size_t)m * (size_t)g.stride * (F32 ? 4 : 2);
     const bool empty = r.m == -inf;
     const double others = empty ? 0.0 : r.s + (double)(r.top - 1), log_s = log1p(others);
-    auto log_p = [&](float x) { return x == -inf ? -inf : (float)(((double)x - (double)r.m) - log_s); };
-    if (tid == 0) {
-        const int token = g.tokens != nullptr ? g.tokens[m] : -1;
-        const bool asked = token >= 0 && token < g.V;
-        if (g.logprob != nullptr) g.logprob[m] = token < 0 ? 0.0f : asked ? log_p(logit_at(row, F32, token)) : -inf;
-        if (g.rank != nullptr) g.rank[m] = token < 0 ? -1 : asked ? r.ahead : g.V;
+    if ((threadIdx.x & 63) == 0) {
+        if (g.logprob != nullptr) g.logprob[m] = a.token < 0 ? 0.0f : a.inside ? log_p(a.mine, r.m, log_s) : -inf;
+        if (g.rank != nullptr) g.rank[m] = a.token < 0 ? -1 : a.inside ? r.ahead : g.V;
         if (g.entropy != nullptr) g.entropy[m] = empty ? 0.0f : (float)(log_s - r.t / (1.0 + others));
     }
+    return log_s;
+}
+
+// The K-th largest order of 64, without its 6 lowest bits, where the lane's
+// number makes all different: a bound from below of the K-th largest logit, if
+// the 64 are maxima of disjoint sets.
+__device__ __forceinline__ uint32_t lane_order(float x) { return (float_order(x) & ~63u) | (threadIdx.x & 63); }
+
+__device__ __forceinline__ float kth_bound(uint32_t mine, const uint32_t (&all)[64], int K)
+{
+    int place = 0;
+#pragma unroll 16
+    for (int j = 0; j < 64; ++j) place += all[j] > mine ? 1 : 0;
+    const int lane = (int)__builtin_ctzll(__ballot(place == K - 1));
+    const uint32_t order = (uint32_t)__builtin_amdgcn_readlane((int)mine, lane) & ~63u;
+    return order > 0x007FFFFFu ? order_float(order) : -__builtin_inff();   // (-inf's order; none below it is a number's)
+}
+
+// A row's outputs, by a workgroup of T threads: sum_of() gives a wave the row's
+// sums (behind the first barrier), largest[] are a thread's groups' maxima,
+// group i * T + thread of those that TW threads of the walk wrote.
+template <bool F32, int T, int TW, typename SumOf>
+__device__ __forceinline__ void finish_row(const LogprobArgs& g, int64_t m, const Asked& a, const float (&largest)[16],
+                                           LogprobLds<T>& lds, SumOf sum_of)
+{
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const float inf = __builtin_inff();
+    const uint8_t* row = row_of<F32>(g, m);
     const int K = g.topk;
-    if (K == 0) return;
-    auto put = [&](int k, float x, int i) {
-        g.topk_ids[m * K + k] = i;
-        g.topk_logprob[m * K + k] = i < 0 ? -inf : log_p(x);
-    };
-    // the bound: the K-th largest of 64 columns' maxima
+    if (K == 0) {
+        __syncthreads();
+        if (wave == T / kWave - 1) finish_sums(g, m, sum_of(), a);
+        return;
+    }
+    float best = largest[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) best = fmaxf(best, largest[i]);
     lds.columns[tid] = best;
     if (tid == 0) lds.n_groups = lds.n_cands = 0;
     __syncthreads();
-    const float column = fmaxf(fmaxf(lds.columns[lane], lds.columns[lane + 64]),
-                               fmaxf(lds.columns[lane + 128], lds.columns[lane + 192]));
-    if (wave == 0) lds.bests[lane] = column;
-    __syncthreads();
-    int place = 0;
+    if (wave == 0) {
+        float column = lds.columns[lane];
 #pragma unroll
-    for (int j = 0; j < 64; ++j) place += logit_before(lds.bests[j], j, column, lane) ? 1 : 0;
-    const float bound = row_lane(column, (int)__builtin_ctzll(__ballot(place == K - 1)));
-    const int n = g.groups * 256;
-    if (best >= bound && best > -inf)
-        for (int i = tid; i < n; i += 256) {
-            const float x = maxima[i];
-            if (x >= bound && x > -inf) {
-                const int at = atomicAdd(&lds.n_groups, 1);
-                if (at < kLogprobGroupList) lds.groups[at] = i;
-            }
+        for (int i = 1; i < T / 64; ++i) column = fmaxf(column, lds.columns[lane + 64 * i]);
+        lds.bests[lane] = lane_order(column);
+    }
+    if (wave == T / kWave - 1) {                         // the sums meanwhile
+        const RowSums r = sum_of();
+        const double log_s = finish_sums(g, m, r, a);
+        if (lane == 0) {
+            lds.m = r.m;
+            lds.log_s = log_s;
         }
+    }
     __syncthreads();
-    const int n_groups = lds.n_groups, each = 16 * g.group_segments;
+    const float bound = kth_bound(lds.bests[lane], lds.bests, K);
+    if (best >= bound && best > -inf) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (largest[i] >= bound && largest[i] > -inf) {
+                const int at = atomicAdd(&lds.n_groups, 1);
+                if (at < kLogprobGroupList) lds.groups[at] = i * T + tid;
+            }
+    }
+    __syncthreads();
+    const int n_groups = lds.n_groups;
     if (n_groups <= kLogprobGroupList) {
-        for (int j = tid; j < n_groups * each; j += 256) {
-            const int group = lds.groups[j / each], in = j % each;
-            const int64_t p = ((int64_t)(group >> 8) * g.group_segments + (in >> 4)) * kLogprobSegment +
-                              ((group & 255) >> 6) * 1024 + logit_place<F32>(group & 63, in & 15);
-            if (p >= g.V) continue;
-            const float x = logit_at(row, F32, (size_t)p);
-            if (x >= bound && x > -inf) {
-                const int at = atomicAdd(&lds.n_cands, 1);
-                if (at < kLogprobCandidates) {
-                    lds.cand_x[at] = x;
-                    lds.cand_i[at] = (int)p;
+        for (int j = tid; j < n_groups * 16; j += T) {
+            const int group = lds.groups[j >> 4], in = j & 15;
+            const int64_t first = (int64_t)(group / TW) * g.group_segments * (16 * TW) + (group % TW >> 6) * 1024 +
+                                  logit_place<F32>(group & 63, in);
+            for (int q = 0; q < g.group_segments; ++q) {
+                const int64_t p = first + q * (16 * TW);
+                if (p >= g.V) break;
+                const float x = logit_at(row, F32, (size_t)p);
+                if (x >= bound && x > -inf) {
+                    const int at = atomicAdd(&lds.n_cands, 1);
+                    if (at < kLogprobCandidates) lds.cands[at] = (uint64_t)float_order(x) << 32 | (uint32_t)~p;
                 }
             }
         }
     }
     __syncthreads();
+    const float row_m = lds.m;
+    const double log_s = lds.log_s;
+    auto put = [&](int k, float x, int i) {
+        g.topk_ids[m * K + k] = i;
+        g.topk_logprob[m * K + k] = i < 0 ? -inf : log_p(x, row_m, log_s);
+    };
     const int n_cands = lds.n_cands;
     if (n_groups <= kLogprobGroupList && n_cands <= kLogprobCandidates) {
-        for (int c = tid; c < n_cands; c += 256) {
-            const float x = lds.cand_x[c];
-            const int i = lds.cand_i[c];
+        for (int c = tid; c < n_cands; c += T) {
+            const uint64_t own = lds.cands[c];
             int at = 0;
-            for (int j = 0; j < n_cands; ++j) at += logit_before(lds.cand_x[j], lds.cand_i[j], x, i) ? 1 : 0;
-            if (at < K) put(at, x, i);
+#pragma unroll 4
+            for (int j = 0; j < n_cands; ++j) at += lds.cands[j] > own ? 1 : 0;
+            if (at < K) put(at, order_float((uint32_t)(own >> 32)), (int)~(uint32_t)own);
         }
-        for (int k = n_cands + tid; k < K; k += 256) put(k, -inf, -1);
+        for (int k = n_cands + tid; k < K; k += T) put(k, -inf, -1);
         return;
     }
     // one after another: the first of those behind the last one
@@ -312,7 +405,7 @@ __device__ __forceinline__ void finish_row(const LogprobArgs& g, int64_t m, cons
         float bx = -inf;
         int bi = -1;
         if (k == 0 || i >= 0) {
-            for (int v = tid; v < g.V; v += 256) {
+            for (int v = tid; v < g.V; v += T) {
                 const float c = logit_at(row, F32, (size_t)v);
                 if (c > -inf && logit_before(x, i, c, v) && (bi < 0 || logit_before(c, v, bx, bi))) {
                     bx = c;
@@ -320,22 +413,22 @@ __device__ __forceinline__ void finish_row(const LogprobArgs& g, int64_t m, cons
                 }
             }
             __syncthreads();
-            lds.cand_x[tid] = bx;
-            lds.cand_i[tid] = bi;
+            lds.best_x[tid] = bx;
+            lds.best_i[tid] = bi;
             __syncthreads();
-            for (int half = 128; half > 0; half >>= 1) {
+            for (int half = T / 2; half > 0; half >>= 1) {
                 if (tid < half) {
-                    const float ox = lds.cand_x[tid + half];
-                    const int oi = lds.cand_i[tid + half];
-                    if (oi >= 0 && (lds.cand_i[tid] < 0 || logit_before(ox, oi, lds.cand_x[tid], lds.cand_i[tid]))) {
-                        lds.cand_x[tid] = ox;
-                        lds.cand_i[tid] = oi;
+                    const float ox = lds.best_x[tid + half];
+                    const int oi = lds.best_i[tid + half];
+                    if (oi >= 0 && (lds.best_i[tid] < 0 || logit_before(ox, oi, lds.best_x[tid], lds.best_i[tid]))) {
+                        lds.best_x[tid] = ox;
+                        lds.best_i[tid] = oi;
                     }
                 }
                 __syncthreads();
             }
-            bx = lds.cand_x[0];
-            bi = lds.cand_i[0];
+            bx = lds.best_x[0];
+            bi = lds.best_i[0];
         }
         x = bx;
         i = bi;
@@ -343,56 +436,69 @@ __device__ __forceinline__ void finish_row(const LogprobArgs& g, int64_t m, cons
     }
 }
 
-// Walks the segments [s0, s1) of a row with the workgroup's four waves, puts
-// the groups' largest logits into `maxima`, and returns the thread's largest;
-// the waves' sums go to LDS.
-template <bool F32>
-__device__ __forceinline__ float walk_row(const LogprobArgs& g, int64_t m, int s0, int s1, float* maxima, LogprobLds& lds)
+// Walks the segments [s0, s1) of a row with the workgroup's T / 64 waves, 1,024
+// logits each, and puts the groups' largest logits into `maxima`.  Returns the
+// wave's sums.
+template <bool F32, int T>
+__device__ __forceinline__ RowSums walk_row(const LogprobArgs& g, int64_t m, int s0, int s1, float* maxima, Asked& a)
 {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     LogitWalk<F32> w;
-    w.row = static_cast<const uint8_t*>(g.logits) + (size_t)m * (size_t)g.stride * (F32 ? 4 : 2);
+    w.row = row_of<F32>(g, m);
     w.V = g.V;
     w.lane = lane;
     Logits16<F32> now, next;
-    auto at = [&](int s) { return s * kLogprobSegment + wave * 1024; };
+    auto at = [&](int s) { return s * (16 * T) + wave * 1024; };
     w.load(at(s0), now);
-    w.token = g.tokens != nullptr ? g.tokens[m] : -1;
-    w.asked = g.rank != nullptr && w.token >= 0 && w.token < g.V;
-    w.mine = w.asked ? logit_at(w.row, F32, w.token) : 0.0f;
+    a = asked_of<F32>(g, m, w.row);
+    w.token = a.token;
+    w.asked = g.rank != nullptr && a.inside;
+    w.mine = a.mine;
     w.above = nextafterf(w.mine, __builtin_inff());
-    float best = -__builtin_inff(), group = best;
+    float group = -__builtin_inff();
     int in = 0;
     for (int s = s0; s < s1; ++s) {
         if (s + 1 < s1) w.load(at(s + 1), next);
         group = fmaxf(group, w.add(at(s), now));
         if (++in == g.group_segments || s + 1 == s1) {
-            if (g.topk > 0) maxima[(s / g.group_segments) * 256 + tid] = group;
-            best = fmaxf(best, group);
+            if (g.topk > 0) maxima[(s / g.group_segments) * T + tid] = group;
             group = -__builtin_inff();
             in = 0;
         }
         now = next;
     }
-    const RowSums r = w.sums();
-    if (lane == 0) lds.parts[wave] = r;
-    return best;
+    return w.sums();
 }
 
 __device__ __forceinline__ RowSums no_sums() { return RowSums{0.0, 0.0, -__builtin_inff(), 0, 0, 0}; }
 
-// A workgroup a row, from the logits to the outputs.
-template <bool F32>
-__global__ __launch_bounds__(256) void logprob_rows_kernel(LogprobArgs g)
+// The largest logits of a thread's groups.
+template <int T>
+__device__ __forceinline__ void load_maxima(const float* maxima, int n, float (&largest)[16])
 {
-    extern __shared__ float maxima[];                    // [groups][256]
-    __shared__ LogprobLds lds;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int at = i * T + (int)threadIdx.x;
+        const float x = maxima[min(at, n - 1)];
+        largest[i] = at < n ? x : -__builtin_inff();
+    }
+}
+
+// A workgroup of T threads a row, from the logits to the outputs.
+template <bool F32, int T>
+__global__ __launch_bounds__(T, 4) void logprob_rows_kernel(LogprobArgs g)
+{
+    extern __shared__ float maxima[];                    // [groups][T]
+    __shared__ LogprobLds<T> lds;
     const int lane = threadIdx.x & 63;
     for (int64_t m = blockIdx.x; m < g.M; m += gridDim.x) {
-        const float best = walk_row<F32>(g, m, 0, g.segments, maxima, lds);
-        __syncthreads();
-        const RowSums r = join_sums(lane < 4 ? lds.parts[lane] : no_sums());
-        finish_row<F32>(g, m, r, best, maxima, lds);
+        Asked a;
+        const RowSums r = walk_row<F32, T>(g, m, 0, g.segments, maxima, a);
+        if (lane == 0) lds.parts[threadIdx.x >> 6] = r;
+        float largest[16] = {};
+        if (g.topk > 0) load_maxima<T>(maxima, g.groups * T, largest);   // (a thread reads what it wrote itself)
+        finish_row<F32, T, T>(g, m, a, largest, lds,
+                              [&] { return join_sums(lane < T / kWave ? lds.parts[lane] : no_sums()); });
         __syncthreads();
     }
 }
@@ -400,31 +506,109 @@ __global__ __launch_bounds__(256) void logprob_rows_kernel(LogprobArgs g)
 // A workgroup a part of a row: its sums and its groups' largest logits go to
 // the workspace.
 template <bool F32>
-__global__ __launch_bounds__(256) void logprob_parts_kernel(LogprobArgs g)
+__global__ __launch_bounds__(256, 5) void logprob_parts_kernel(LogprobArgs g)
 {
-    __shared__ LogprobLds lds;
+    __shared__ RowSums parts[4];
     const int lane = threadIdx.x & 63;
     const int64_t m = blockIdx.x / g.parts;
     const int part = (int)(blockIdx.x - m * g.parts), s0 = part * g.part_segments;
-    walk_row<F32>(g, m, s0, min(s0 + g.part_segments, g.segments), g.maxima + m * g.groups * 256, lds);
+    Asked a;
+    const RowSums r = walk_row<F32, 256>(g, m, s0, min(s0 + g.part_segments, g.segments), g.maxima + m * g.groups * 256, a);
+    if (lane == 0) parts[threadIdx.x >> 6] = r;
     __syncthreads();
-    const RowSums r = join_sums(lane < 4 ? lds.parts[lane] : no_sums());
-    if (threadIdx.x == 0) g.sums[m * g.parts + part] = r;
+    if (threadIdx.x >= 64) return;
+    const RowSums all = join_sums(lane < 4 ? parts[lane] : no_sums());
+    if (lane == 0) g.sums[m * g.parts + part] = all;
 }
 
-// A workgroup a row, from its parts to the outputs.
+// A workgroup a row (a wave, where no alternatives are asked for), from its
+// parts to the outputs.
 template <bool F32>
-__global__ __launch_bounds__(256) void logprob_join_kernel(LogprobArgs g)
+__global__ __launch_bounds__(1024) void logprob_join_kernel(LogprobArgs g)
 {
-    __shared__ LogprobLds lds;
-    const int tid = threadIdx.x, lane = tid & 63;
+    __shared__ LogprobLds<1024> lds;
+    const int lane = threadIdx.x & 63;
     const int64_t m = blockIdx.x;
-    const float* maxima = g.maxima + m * g.groups * 256;
-    float best = -__builtin_inff();
-    if (g.topk > 0)
-        for (int i = tid; i < g.groups * 256; i += 256) best = fmaxf(best, maxima[i]);
-    const RowSums r = join_sums(lane < g.parts ? g.sums[m * g.parts + lane] : no_sums());
-    finish_row<F32>(g, m, r, best, maxima, lds);
+    float largest[16] = {};
+    const Asked a = asked_of<F32>(g, m, row_of<F32>(g, m));
+    const RowSums mine = lane < g.parts ? g.sums[m * g.parts + lane] : no_sums();
+    if (g.topk == 0) {
+        finish_sums(g, m, join_sums(mine), a);
+        return;
+    }
+    load_maxima<1024>(g.maxima + m * g.groups * 256, g.groups * 256, largest);
+    finish_row<F32, 1024, 256>(g, m, a, largest, lds, [&] { return join_sums(mine); });
+}
+
+// A wave a row of at most 1,024 logits: they stay in its registers, and its
+// lanes' maxima bound the alternatives.
+template <bool F32>
+__global__ __launch_bounds__(256, 4) void logprob_short_kernel(LogprobArgs g)
+{
+    __shared__ uint32_t bests[4][64];
+    __shared__ uint64_t cands[4][kLogprobShortList];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const float inf = __builtin_inff();
+    const int64_t m = (int64_t)blockIdx.x * 4 + wave;
+    if (m >= g.M) return;
+    LogitWalk<F32> w;
+    w.row = row_of<F32>(g, m);
+    w.V = g.V;
+    w.lane = lane;
+    Logits16<F32> raw;
+    w.load(0, raw);
+    const Asked a = asked_of<F32>(g, m, w.row);
+    w.token = a.token;
+    w.asked = g.rank != nullptr && a.inside;
+    w.mine = a.mine;
+    w.above = nextafterf(w.mine, inf);
+    const float best = w.add(0, raw);
+    const RowSums r = w.sums();
+    const double log_s = finish_sums(g, m, r, a);
+    const int K = g.topk;
+    if (K == 0) return;
+    auto put = [&](int k, float x, int i) {
+        g.topk_ids[m * K + k] = i;
+        g.topk_logprob[m * K + k] = i < 0 ? -inf : log_p(x, r.m, log_s);
+    };
+    bests[wave][lane] = lane_order(best);
+    __builtin_amdgcn_wave_barrier();
+    const float bound = kth_bound(bests[wave][lane], bests[wave], K);
+    int n = 0;
+    uint64_t keys[16];                                   // 0: not a candidate
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float x = logit_value(raw.get(i));
+        const int p = logit_place<F32>(lane, i);
+        const bool in = p < g.V && x >= bound && x > -inf;
+        keys[i] = in ? (uint64_t)float_order(x) << 32 | (uint32_t)~p : 0;
+        const uint64_t who = __ballot(in);
+        const int at = n + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
+        if (in && at < kLogprobShortList) cands[wave][at] = keys[i];
+        n += __popcll(who);
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (n <= kLogprobShortList) {
+        for (int c = lane; c < n; c += 64) {
+            const uint64_t own = cands[wave][c];
+            int at = 0;
+#pragma unroll 4
+            for (int j = 0; j < n; ++j) at += cands[wave][j] > own ? 1 : 0;
+            if (at < K) put(at, order_float((uint32_t)(own >> 32)), (int)~(uint32_t)own);
+        }
+        for (int k = n + lane; k < K; k += 64) put(k, -inf, -1);
+        return;
+    }
+    // (equal logits) the largest key left, K times
+    for (int k = 0; k < K; ++k) {
+        uint64_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = max_u64(top, keys[i]);
+        top = wave_max_u64(top);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) keys[i] = keys[i] == top ? 0 : keys[i];
+        if (lane == 0) put(k, order_float((uint32_t)(top >> 32)), (int)~(uint32_t)top);
+    }
 }
 
 }  // namespace moe

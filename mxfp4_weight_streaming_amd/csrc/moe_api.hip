@@ -1048,6 +1048,8 @@ moe_status moe_token_logprobs(int32_t M, int32_t V, const void* logits, int32_t 
     a.type = logits_type;
     a.topk = topk;
     hipError_t e = moe::launch_logprobs(a, static_cast<hipStream_t>(stream));
+    if (e == hipErrorInvalidConfiguration)
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%d rows are more than one launch takes", M);
     return e == hipSuccess ? MOE_OK : hip_fail(e, "log probability launch");
 }
 
