@@ -13,8 +13,8 @@ namespace moe {
 
 // ---- log probabilities -----------------------------------------------------------
 // Each wave walks a row 1,024 logits at a time.  Rows of at most 1,024 have a
-// wave each; others a workgroup of 256, 512 or 1,024 threads, as many as give
-// every compute unit 16 waves; and where rows are too few for that, they are
+// wave each; others a workgroup of 256, 512 or 1,024 threads, the most with
+// which all rows' waves are resident at once, 16 a compute unit; and where rows are too few for that, they are
 // split into parts of 256 threads, joined by a second kernel.
 constexpr int kLogprobMaxParts = 64;            // one lane each where they are joined
 constexpr int kLogprobShort = 1024;
@@ -34,7 +34,7 @@ constexpr LogprobPlan logprob_plan(int64_t M, int V)
     const bool split = M <= kLogprobSplitRows && V > 16 * 1024;
     p.threads = 256;
     // (no more waves than there are segments for)
-    while (!split && p.threads < 1024 && M * p.threads / 64 < kLogprobWaves && V > 16 * p.threads) p.threads *= 2;
+    while (!split && p.threads < 1024 && M * p.threads / 64 * 2 <= kLogprobWaves && V > 16 * p.threads) p.threads *= 2;
     p.segments = (int)ceil_div(V, 16 * p.threads);
     // the threads that read the groups' maxima hold 16 each: 1,024 of a row in
     // parts, else those that wrote them

@@ -31,6 +31,7 @@ constexpr int kLogprobGroupList = 256;      // groups read again
 constexpr int kLogprobCandidates = 512;     // logits ranked
 constexpr int kLogprobShortList = 128;      // ... of a row that one wave holds
 
+constexpr float kLog2e = 1.44269504f;
 constexpr float kLargestLogit = 3.40282347e38f;
 
 // A logit's value as the definitions count it.
@@ -145,10 +146,24 @@ struct LogitWalk {
     int token;
     bool asked;
     float mine, above;                                   // its logit, and the next larger number
-    // state: s and t a lane, the rest the wave's
+    // state: s = sum 2^z and t = sum 2^z z a lane, with z = log2(e) l - ref; the
+    // rest the wave's: m its largest, `top` logits equal to it and not in s
     double s = 0.0, t = 0.0;
-    float m = -__builtin_inff();
+    float m = -__builtin_inff(), ref = 0.0f;
     int top = 0, ahead = 0;
+
+    // log2(e) m - ref, which is 0 but for ref's rounding
+    __device__ __forceinline__ double off() const { return (double)m * (double)kLog2e - (double)ref; }
+
+    // Brings the sums to a new reference; d = the old one less the new one.
+    __device__ __forceinline__ void rebase(double d)
+    {
+        if (s != 0.0) {                                  // (d may be infinite, and a NaN where s is 0)
+            const double f = exp(d * 0.69314718055994531);
+            t = f == 0.0 ? 0.0 : (t + s * d) * f;
+            s *= f;
+        }
+    }
 
     __device__ __forceinline__ void load(int at, Logits16<F32>& x) const
     {
@@ -197,13 +212,18 @@ struct LogitWalk {
                 most = kLargestLogit;
             }
             if (most > m) {
+                // (never -inf itself: z of -inf would be +inf)
+                const float to = fmaxf(most * kLog2e, -kLargestLogit);
                 if (m > -inf) {
-                    if (lane == 0) s += (double)top;
-                    const double d = (double)m - (double)most, f = exp(d);
-                    t = (t + s * d) * f;
-                    s *= f;
+                    const float z = (float)off(), e = __builtin_amdgcn_exp2f(z);
+                    if (lane == 0 && e != 0.0f) {
+                        s += (double)top * (double)e;
+                        t += (double)top * (double)e * (double)z;
+                    }
+                    rebase((double)ref - (double)to);
                 }
                 m = most;
+                ref = to;
                 top = 0;
             }
             equal = true;
@@ -213,14 +233,14 @@ struct LogitWalk {
             auto sums = [&](auto exclude) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float y = fmaxf(x[i] - m, -256.0f);
-                    float e = __builtin_amdgcn_exp2f(y * 1.44269504f);
+                    const float z = fmaxf(fmaf(x[i], kLog2e, -ref), -256.0f);
+                    float e = __builtin_amdgcn_exp2f(z);
                     if constexpr (decltype(exclude)::value) {
                         top += __popcll(__ballot(x[i] == m));
                         e = x[i] == m ? 0.0f : e;
                     }
                     ss[i & 3] += e;
-                    tt[i & 3] = fmaf(e, y, tt[i & 3]);
+                    tt[i & 3] = fmaf(e, z, tt[i & 3]);
                 }
             };
             if (equal) sums(std::true_type{});
@@ -249,9 +269,13 @@ struct LogitWalk {
         return largest;
     }
 
-    __device__ __forceinline__ RowSums sums() const
+    // The wave's sums at the reference m, in natural logarithms.
+    __device__ __forceinline__ RowSums sums()
     {
-        return RowSums{wave_sum_f64(s), wave_sum_f64(t), m, top, ahead, 0};
+        s = wave_sum_f64(s);
+        t = wave_sum_f64(t);
+        rebase(-off());
+        return RowSums{s, t * 0.69314718055994531, m, top, ahead, 0};
     }
 };
 
