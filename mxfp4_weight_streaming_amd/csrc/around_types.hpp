@@ -80,9 +80,12 @@ struct LoraArgs {
     const int32_t* ids;      // [M]
     const void* base;        // [M, N] or nullptr (0)
     void* out;               // [M, N]
-    float* u;                // [M, r], workspace
+    float* u;                // [M, rp], workspace
     int64_t M, N;
-    int K, r, L, base_type, out_type;
+    int K, r, rp, L, out_type;   // rp: r up to a multiple of 32; base is of out's type
+    // by the launcher: workgroups that share a tile's adapters, and tiles of 16
+    // tokens a workgroup takes
+    int slots, token_tiles;
 };
 
 }  // namespace moe

@@ -46,4 +46,29 @@ constexpr LogprobPlan logprob_plan(int64_t M, int V)
     return p;
 }
 
+// ---- adapters ------------------------------------------------------------------
+constexpr int lora_padded(int r) { return (r + 31) / 32 * 32; }   // ranks of a row of u
+
+struct LoraPlan {
+    int shrink_slots, expand_slots, token_tiles;
+};
+
+// The adapters of a tile of 16 tokens are dealt to so many workgroups that there
+// are about 2,048 of them (at most 16: a token each).
+constexpr int lora_slots(int64_t tiles)
+{
+    int slots = 1;
+    while (slots < 16 && tiles * slots < 1024) slots *= 2;
+    return slots;
+}
+
+constexpr LoraPlan lora_plan(int64_t M, int64_t N, int r)
+{
+    LoraPlan p{};
+    p.shrink_slots = lora_slots(ceil_div(M, 16) * (lora_padded(r) / 16));
+    p.token_tiles = 1;
+    p.expand_slots = lora_slots(ceil_div(M, 16) * ceil_div(N, 256));
+    return p;
+}
+
 }  // namespace moe

@@ -3,7 +3,9 @@
 // summed exactly in int32, so no order of the sum changes the result.
 #pragma once
 
-#include "around_common.hpp"
+#include <type_traits>
+
+#include "lora_common.hpp"
 
 namespace moe {
 
@@ -76,9 +78,34 @@ __device__ __forceinline__ int32_t dot16(u32x4 a, u32x4 b, int32_t acc)
     return __builtin_amdgcn_sdot4((int)a.w, (int)b.w, acc, false);
 }
 
-template <int MT, int U, int L, int R>
-__global__ __launch_bounds__(256) void int8_gemv_kernel(Int8Args g)
+// Products alone, or with the tokens' adapters added (LoraArgs, u computed).
+struct NoAdapters {};
+
+template <int L>
+__device__ __forceinline__ float group_sum_f32(float v)
 {
+    if constexpr (L == 16) return group_sum<16>(v);
+    else return wave_sum(v);
+}
+
+// sum_j B[i][n, j] u[j] of a token's adapter, by the L lanes of a channel; 0
+// where it has none.
+template <int L>
+__device__ __forceinline__ float gemv_delta(const LoraArgs& a, int t, int64_t n, int li)
+{
+    const int i = adapter_of(a, t);
+    float d = 0.0f;
+    if (i >= 0) {
+        const uint16_t* b = a.b + ((size_t)i * a.N + n) * a.r;
+        for (int j = li; j < a.r; j += L) d = fmaf(a.u[t * a.rp + j], bf16_bits_to_f32(b[j]), d);
+    }
+    return group_sum_f32<L>(d);
+}
+
+template <int MT, int U, int L, int R, typename Adapters = NoAdapters>
+__global__ __launch_bounds__(256) void int8_gemv_kernel(Int8Args g, Adapters ad)
+{
+    constexpr bool LORA = !std::is_same<Adapters, NoAdapters>::value;
     extern __shared__ u32x4 xs[];                        // [token][padded chunk]
     constexpr int CH = 4 * R * (64 / L);                 // channels a workgroup holds
     const int M = (int)g.M, K = g.K, chunks = (K + 15) / 16;
@@ -147,8 +174,11 @@ __global__ __launch_bounds__(256) void int8_gemv_kernel(Int8Args g)
                     if (t >= M) continue;
                     const int32_t sum = group_sum_i32<L>(acc[r][t]);
                     acc[r][t] = 0;
+                    float delta = 0.0f;
+                    if constexpr (LORA) delta = gemv_delta<L>(ad, t, min(n, g.N - 1), li);
                     if (li == 0 && n < g.N) {
-                        const float v = int8_scaled(sum, g.a_scale[t], ws);
+                        float v = int8_scaled(sum, g.a_scale[t], ws);
+                        if constexpr (LORA) v += delta;
                         if (g.out_type == kTypeF32) static_cast<float*>(g.out)[(size_t)t * g.N + n] = v;
                         else static_cast<uint16_t*>(g.out)[(size_t)t * g.N + n] = (uint16_t)f32_to_bf16_bits(v);
                     }
@@ -221,14 +251,47 @@ __device__ __forceinline__ void wait_steps(int steps)
     }
 }
 
+// The adapters' part of 16 tokens (the lane's is m) and FN x 16 channels from n0,
+// as the products above hold them: rows of B are the first operand, so a lane
+// gets channels 4 (l / 16) + 0..3 of tile j.
+template <int FN>
+__device__ __forceinline__ void tile_delta(const LoraArgs& a, int64_t m, int64_t n0, f32x4 (&delta)[FN])
+{
+    const int lane = threadIdx.x & 63, row = lane & 15, k0 = (lane >> 4) * 8;
+    const bool even = a.r % 8 == 0;
+    const float* u = a.u + (size_t)min(m, a.M - 1) * a.rp + k0;
+    each_adapter(adapter_of(a, m), 0, 1, [&](int i, bool mine) {
+        if (i < 0) return;
+        f32x4 acc[FN] = {};
+        for (int k = 0; k < a.rp; k += 32) {
+            u32x4 bv[FN];
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                const uint16_t* b = a.b + ((size_t)i * a.N + min(n0 + j * 16 + row, a.N - 1)) * a.r;
+                bv[j] = even ? load_bf16x8<true>(b, k + k0, a.r) : load_bf16x8<false>(b, k + k0, a.r);
+            }
+            const Split3 s = split_u(u + k);
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int p = 2; p >= 0; --p) acc[j] = mfma(bv[j], s.v[p], acc[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) delta[j][e] += mine ? acc[j][e] : 0.0f;
+    });
+}
+
 template <int N>
 struct Count {
     static constexpr int value = N;
 };
 
-template <int BM, int BN, int WM, int WN, int BK, int S, int EU, bool DIRECT>
-__global__ __launch_bounds__(64 * WM * WN, EU) void int8_tile_kernel(Int8Args g)
+template <int BM, int BN, int WM, int WN, int BK, int S, int EU, bool DIRECT, typename Adapters = NoAdapters>
+__global__ __launch_bounds__(64 * WM * WN, EU) void int8_tile_kernel(Int8Args g, Adapters ad)
 {
+    constexpr bool LORA = !std::is_same<Adapters, NoAdapters>::value;
     constexpr int T = 64 * WM * WN, FM = BM / (16 * WM), FN = BN / (16 * WN), CR = BK / 16;
     constexpr int ROWS = BM + BN, NL = ROWS * CR / T;    // rows in LDS, chunks a thread loads a step
     static_assert(BM % (16 * WM) == 0 && BN % (16 * WN) == 0 && ROWS * CR % T == 0 && BM % (T / CR) == 0, "tile shape");
@@ -405,6 +468,8 @@ __global__ __launch_bounds__(64 * WM * WN, EU) void int8_tile_kernel(Int8Args g)
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         const int64_t m = m0 + (wm * FM + i) * 16 + row;
+        f32x4 delta[LORA ? FN : 1] = {};
+        if constexpr (LORA) tile_delta<FN>(ad, m, n0 + wn * FN * 16, delta);
         if (m >= g.M) continue;
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
@@ -413,6 +478,9 @@ __global__ __launch_bounds__(64 * WM * WN, EU) void int8_tile_kernel(Int8Args g)
             float o[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) o[r] = int8_scaled(acc[j][i][r], as[i], ws[j][r]);
+            if constexpr (LORA)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) o[r] += delta[j][r];
             const size_t p = (size_t)m * g.N + n;
             const bool all = n + 4 <= g.N;               // a row may start at any address
             if (g.out_type == kTypeF32) {
