@@ -50,11 +50,12 @@ constexpr LogprobPlan logprob_plan(int64_t M, int V)
 constexpr int lora_padded(int r) { return (r + 31) / 32 * 32; }   // ranks of a row of u
 
 struct LoraPlan {
+    bool few, fused, shrink_few;
     int shrink_slots, expand_slots, token_tiles;
 };
 
 // The adapters of a tile of 16 tokens are dealt to so many workgroups that there
-// are about 2,048 of them (at most 16: a token each).
+// are about 1,024 of them (at most 16: a token each).
 constexpr int lora_slots(int64_t tiles)
 {
     int slots = 1;
@@ -62,12 +63,20 @@ constexpr int lora_slots(int64_t tiles)
     return slots;
 }
 
-constexpr LoraPlan lora_plan(int64_t M, int64_t N, int r)
+constexpr int kLoraFewTokens = 64;
+constexpr int64_t kLoraFusedWork = 65536;   // values of an adapter's A
+
+constexpr LoraPlan lora_plan(int64_t M, int64_t N, int64_t K, int r)
 {
     LoraPlan p{};
-    p.shrink_slots = lora_slots(ceil_div(M, 16) * (lora_padded(r) / 16));
+    p.few = M <= kLoraFewTokens;
+    p.fused = p.few && K % 8 == 0 && r * K <= kLoraFusedWork && M * ceil_div(N, 256) <= kCus;
+    p.shrink_few = M <= kLoraFewTokens;
+    p.shrink_slots = lora_slots(ceil_div(M, 16) * ceil_div(r, r > 16 ? 32 : 16));
+    const int64_t tn = ceil_div(N, 256), tm = ceil_div(M, 16);
     p.token_tiles = 1;
-    p.expand_slots = lora_slots(ceil_div(M, 16) * ceil_div(N, 256));
+    while (p.token_tiles < 4 && ceil_div(tm, 2 * p.token_tiles) * tn >= 2 * kCus) p.token_tiles *= 2;
+    p.expand_slots = p.token_tiles == 1 ? lora_slots(tm * tn) : 1;
     return p;
 }
 

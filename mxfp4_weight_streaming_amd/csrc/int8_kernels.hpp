@@ -251,37 +251,116 @@ __device__ __forceinline__ void wait_steps(int steps)
     }
 }
 
-// The adapters' part of 16 tokens (the lane's is m) and FN x 16 channels from n0,
-// as the products above hold them: rows of B are the first operand, so a lane
-// gets channels 4 (l / 16) + 0..3 of tile j.
-template <int FN>
-__device__ __forceinline__ void tile_delta(const LoraArgs& a, int64_t m, int64_t n0, f32x4 (&delta)[FN])
-{
-    const int lane = threadIdx.x & 63, row = lane & 15, k0 = (lane >> 4) * 8;
-    const bool even = a.r % 8 == 0;
-    const float* u = a.u + (size_t)min(m, a.M - 1) * a.rp + k0;
-    each_adapter(adapter_of(a, m), 0, 1, [&](int i, bool mine) {
-        if (i < 0) return;
-        f32x4 acc[FN] = {};
-        for (int k = 0; k < a.rp; k += 32) {
-            u32x4 bv[FN];
+// The adapters' part of a tile's FM x 16 tokens and FN x 16 channels, as the
+// products above hold them: rows of B are the first operand, so a lane gets
+// channels 4 (l / 16) + 0..3 of tile j and one token.  What it takes from
+// memory (the tokens' adapters and u, B's rows) is asked for as early as it can
+// be: one token tile after another, each would be a round trip or two.
+template <int FM, int FN>
+struct TileAdapters {
+    // B's rows of G adapters together: 16 tokens of a decode batch may have as many
+    static constexpr int G = FM * FN <= 2 ? 4 : FM * FN <= 4 ? 2 : 1;
+    const LoraArgs& a;
+    int64_t m0, n0;
+    int row, k0, ids[FM];
+    f32x4 u[FM][2];                                      // of the first 32 ranks
+    u32x4 bv[G][FN];
+    int held = -1;                                       // the adapter whose first 32 ranks bv[0] has
+
+    __device__ __forceinline__ TileAdapters(const LoraArgs& args, int64_t m, int64_t n) : a(args), m0(m), n0(n)
+    {
+        const int lane = threadIdx.x & 63;
+        row = lane & 15;
+        k0 = (lane >> 4) * 8;
 #pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                const uint16_t* b = a.b + ((size_t)i * a.N + min(n0 + j * 16 + row, a.N - 1)) * a.r;
-                bv[j] = even ? load_bf16x8<true>(b, k + k0, a.r) : load_bf16x8<false>(b, k + k0, a.r);
-            }
-            const Split3 s = split_u(u + k);
+        for (int i = 0; i < FM; ++i) ids[i] = adapter_of(a, m0 + i * 16 + row);
+        load_u(0, 0, u[0]);
+    }
+
+    __device__ __forceinline__ void load_u(int i, int k, f32x4 (&v)[2]) const
+    {
+        const f32x4* p = reinterpret_cast<const f32x4*>(a.u + (size_t)min(m0 + i * 16 + row, a.M - 1) * a.rp + k0 + k);
+        v[0] = p[0];
+        v[1] = p[1];
+    }
+
+    __device__ __forceinline__ void load_b(int adapter, int k, u32x4 (&v)[FN]) const
+    {
 #pragma unroll
-            for (int j = 0; j < FN; ++j)
-#pragma unroll
-                for (int p = 2; p >= 0; --p) acc[j] = mfma(bv[j], s.v[p], acc[j]);
+        for (int j = 0; j < FN; ++j) {
+            const uint16_t* b = a.b + ((size_t)adapter * a.N + min(n0 + j * 16 + row, a.N - 1)) * a.r;
+            v[j] = a.r % 8 == 0 ? load_bf16x8<true>(b, k + k0, a.r) : load_bf16x8<false>(b, k + k0, a.r);
         }
+    }
+
+    __device__ __forceinline__ void add(const u32x4 (&s)[3], const u32x4 (&v)[FN], f32x4 (&acc)[FN]) const
+    {
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) delta[j][e] += mine ? acc[j][e] : 0.0f;
-    });
-}
+            for (int p = 2; p >= 0; --p) acc[j] = mfma(v[j], s[p], acc[j]);
+    }
+
+    __device__ __forceinline__ void split(const f32x4 (&v)[2], u32x4 (&s)[3]) const
+    {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const Split3 q = split_pair(v[e >> 1][e & 1 ? 2 : 0], v[e >> 1][e & 1 ? 3 : 1]);
+#pragma unroll
+            for (int p = 0; p < 3; ++p) s[p][e] = q.v[p];
+        }
+    }
+
+    // Token tile i, in turn.
+    __device__ __forceinline__ void delta(int i, f32x4 (&d)[FN])
+    {
+        if (i + 1 < FM) load_u(i + 1, 0, u[i + 1]);
+        uint32_t todo = (uint32_t)__ballot(ids[i] >= 0) & 0xFFFFu;
+        while (todo != 0) {
+            int which[G], n = 0;
+#pragma unroll
+            for (int q = 0; q < G; ++q) {
+                which[q] = -1;
+                if (todo != 0) {
+                    which[q] = __builtin_amdgcn_readlane(ids[i], (int)__builtin_ctz(todo));
+                    todo &= ~(uint32_t)__ballot(ids[i] == which[q]);
+                    ++n;
+                }
+            }
+            f32x4 acc[G][FN] = {};
+            for (int k = 0; k < a.rp; k += 32) {
+                if (k > 0 || held != which[0] || n > 1) {
+#pragma unroll
+                    for (int q = 0; q < G; ++q)
+                        if (q < n) load_b(which[q], k, bv[q]);
+                    held = k == 0 ? which[0] : -1;
+                }
+                u32x4 s[3];
+                if (k == 0) {
+                    split(u[i], s);
+                } else {
+                    f32x4 v[2];
+                    load_u(i, k, v);
+                    split(v, s);
+                }
+#pragma unroll
+                for (int q = 0; q < G; ++q)
+                    if (q < n) add(s, bv[q], acc[q]);
+            }
+#pragma unroll
+            for (int q = 0; q < G; ++q)
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) d[j][e] += q < n && ids[i] == which[q] ? acc[q][j][e] : 0.0f;
+        }
+    }
+};
+
+struct NoTileAdapters {
+    template <typename... T>
+    __device__ __forceinline__ NoTileAdapters(const T&...) {}
+};
 
 template <int N>
 struct Count {
@@ -329,11 +408,11 @@ __global__ __launch_bounds__(64 * WM * WN, EU) void int8_tile_kernel(Int8Args g,
     auto base = [&](int j) { return j * (T / CR) < BM ? a0 : w0; };
     auto buf = [&](int i) { return lds + i * (ROWS * CR); };
 
+    const int row = lane & 15;
     i32x4 acc[FN][FM] = {};
     struct Frags {
         i32x4 op[FN + FM];                               // operands of 64 codes: channels, then tokens
     };
-    const int row = lane & 15;
     auto read = [&](Frags& f, const u32x4* b, int kk, int i) {
         const int c = (kk * 4 + (lane >> 4)) ^ int8_swizzle<BK>(row);
         const int r = i < FN ? BM + (wn * FN + i) * 16 : (wm * FM + i - FN) * 16;
@@ -455,6 +534,8 @@ __global__ __launch_bounds__(64 * WM * WN, EU) void int8_tile_kernel(Int8Args g,
         }
     }
 
+    typename std::conditional<LORA, TileAdapters<FM, FN>, NoTileAdapters>::type tile_adapters(
+        ad, m0 + wm * FM * 16, n0 + wn * FN * 16);
     // every scale is loaded before the first store: a store may change what a
     // later load reads, for all the compiler knows, so loads among the stores
     // would wait one by one
@@ -469,7 +550,10 @@ __global__ __launch_bounds__(64 * WM * WN, EU) void int8_tile_kernel(Int8Args g,
     for (int i = 0; i < FM; ++i) {
         const int64_t m = m0 + (wm * FM + i) * 16 + row;
         f32x4 delta[LORA ? FN : 1] = {};
-        if constexpr (LORA) tile_delta<FN>(ad, m, n0 + wn * FN * 16, delta);
+        if constexpr (LORA) {
+            __builtin_amdgcn_sched_barrier(0);           // (one tile's registers at a time)
+            tile_adapters.delta(i, delta);
+        }
         if (m >= g.M) continue;
 #pragma unroll
         for (int j = 0; j < FN; ++j) {

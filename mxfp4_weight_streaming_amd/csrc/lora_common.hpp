@@ -24,6 +24,7 @@ namespace moe {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef u32x4 u32x4_half __attribute__((aligned(2)));    // at any bf16
+typedef u32x2 u32x2_half __attribute__((aligned(2)));
 typedef f32x4 f32x4_word __attribute__((aligned(4)));    // at any fp32
 
 // The adapter of token m, or -1; -2 for what is no token.
@@ -34,7 +35,7 @@ __device__ __forceinline__ int adapter_of(const LoraArgs& g, int64_t m)
     return i >= 0 && i < g.L ? i : -1;
 }
 
-// Calls f(adapter, whether the lane's token has it) for each adapter among the
+// Calls f(adapter, mask of the tokens that have it) for each adapter among the
 // wave's 16 tokens (-1, none, too) that falls to `slot` of `slots` (a power of
 // two).
 template <typename F>
@@ -43,8 +44,9 @@ __device__ __forceinline__ void each_adapter(int id, int slot, int slots, F f)
     uint32_t todo = (uint32_t)__ballot(id >= -1) & 0xFFFFu;
     for (int d = 0; todo != 0; ++d) {
         const int i = __builtin_amdgcn_readlane(id, (int)__builtin_ctz(todo));
-        todo &= ~(uint32_t)__ballot(id == i);
-        if ((d & (slots - 1)) == slot) f(i, id == i);
+        const uint32_t mask = (uint32_t)__ballot(id == i) & 0xFFFFu;
+        todo &= ~mask;
+        if ((d & (slots - 1)) == slot) f(i, mask);
     }
 }
 
@@ -58,13 +60,26 @@ __device__ __forceinline__ u32x4 load_bf16x8(const uint16_t* row, int k, int n)
         return k < n ? v : u32x4{0, 0, 0, 0};
     }
     const uint16_t* p = row + k;
-    n -= k;
-    if (n >= 8) return *reinterpret_cast<const u32x4_half*>(p);
+    if (k + 8 <= n) return *reinterpret_cast<const u32x4_half*>(p);
     uint32_t d[4] = {0, 0, 0, 0};
+    if (k < n)
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
-        if (i < n) d[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+        for (int i = 0; i < 7; ++i) {                    // (all asked for at once)
+            const uint32_t v = p[min(i, n - 1 - k)];
+            d[i >> 1] |= (k + i < n ? v : 0) << (16 * (i & 1));
+        }
     return u32x4{d[0], d[1], d[2], d[3]};
+}
+
+// acc + the sum of 8 products, one after another in fp32.
+__device__ __forceinline__ float dot8(u32x4 a, u32x4 b, float acc)
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        acc = fmaf(__uint_as_float(a[e] << 16), __uint_as_float(b[e] << 16), acc);
+        acc = fmaf(__uint_as_float(a[e] & 0xFFFF0000u), __uint_as_float(b[e] & 0xFFFF0000u), acc);
+    }
+    return acc;
 }
 
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c)
@@ -72,26 +87,21 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c)
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// u[0 .. 7] as three bf16 numbers that add up to each value.
+// Two fp32 values as three pairs of bf16 that add up to them.
 struct Split3 {
-    u32x4 v[3];
+    uint32_t v[3];
 };
 
-__device__ __forceinline__ Split3 split_u(const float* u)
+__device__ __forceinline__ Split3 split_pair(float a, float b)
 {
-    const f32x4* q = reinterpret_cast<const f32x4*>(u);
-    const f32x4 a = q[0], b = q[1];
-    float f[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
     Split3 s;
 #pragma unroll
-    for (int p = 0; p < 3; ++p)
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            const uint32_t lo = f32_to_bf16_bits(f[i]), hi = f32_to_bf16_bits(f[i + 1]);
-            s.v[p][i >> 1] = lo | hi << 16;
-            f[i] -= bf16_bits_to_f32(lo);
-            f[i + 1] -= bf16_bits_to_f32(hi);
-        }
+    for (int p = 0; p < 3; ++p) {
+        const uint32_t lo = f32_to_bf16_bits(a), hi = f32_to_bf16_bits(b);
+        s.v[p] = lo | hi << 16;
+        a -= bf16_bits_to_f32(lo);
+        b -= bf16_bits_to_f32(hi);
+    }
     return s;
 }
 

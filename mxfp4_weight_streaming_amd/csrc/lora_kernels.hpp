@@ -6,101 +6,196 @@
 
 namespace moe {
 
+// u of ranks k .. k + 3 of a token, zeros behind r; the 16 behind a last tile
+// that ends in the middle of 32 are cleared with it.
+__device__ __forceinline__ void store_u(const LoraArgs& g, int64_t m, int k, f32x4 u)
+{
+    if (k >= g.rp) return;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) u[e] = k + e < g.r ? u[e] : 0.0f;
+    f32x4* p = reinterpret_cast<f32x4*>(g.u + (size_t)m * g.rp + k);
+    p[0] = u;
+    if (k / 16 * 16 + 16 >= g.r && k + 16 < g.rp) p[4] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+}
+
 // ---------------------------------------------------------------------------
-// u of 16 tokens and 16 rows of A: 8 waves share K, their sums meet in LDS.
+// u of 16 tokens and RR x 16 rows of A: 8 waves share K, 64 values at a time,
+// and their sums meet in LDS.  A matrix operand wants 16 rows side by side in
+// neighbouring lanes, which as loads are 16 lines of memory at 16 bytes each (a
+// lane a clock: 2,048 tokens of rank 64 16 us); here 8 lanes read a row's 128
+// bytes, and the operands are read back from the wave's own 2 KB of LDS a tile
+// (chunk c of row r at c ^ r % 8, so that neither side has bank conflicts).
 // ---------------------------------------------------------------------------
+template <int RR>
 __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs g)
 {
-    constexpr int W = 8, U = 5;                          // waves; steps of 32 whose loads go out together
-    __shared__ f32x4 part[W][64];
+    constexpr int W = 8, U = 5;                          // waves, and chunks of 64 whose loads are in flight
+    __shared__ u32x4 stage[W][1 + RR][16 * 8];
+    __shared__ f32x4 part[W][RR][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int row = lane & 15, k0 = (lane >> 4) * 8;
-    const int ranks = g.rp / 16, slot = (int)(blockIdx.x % g.slots);
-    const int64_t rest = blockIdx.x / g.slots, m0 = rest / ranks * 16;
-    const int r0 = (int)(rest % ranks) * 16;
+    const int row = lane & 15, quarter = lane >> 4, load_row = lane >> 3, chunk = lane & 7;
+    const int ranks = (g.r + 16 * RR - 1) / (16 * RR);
+    // (workgroups go to the 8 XCDs in turn: slots, most of them idle, come last)
+    const int64_t tiles = (g.M + 15) / 16 * ranks, tile = blockIdx.x % tiles, m0 = tile / ranks * 16;
+    const int slot = (int)(blockIdx.x / tiles), r0 = (int)(tile % ranks) * 16 * RR;
     const int id = adapter_of(g, m0 + row);
-    const uint16_t* x = g.x + (size_t)min(m0 + row, g.M - 1) * g.K;
-    const int whole = g.K / 32, s0 = whole * wave / W, s1 = whole * (wave + 1) / W;
-    each_adapter(id, slot, g.slots, [&](int i, bool mine) {
+    const uint16_t* x[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) x[h] = g.x + (size_t)min(m0 + h * 8 + load_row, g.M - 1) * g.K;
+    const int chunks = g.K / 64, s0 = chunks * wave / W, s1 = chunks * (wave + 1) / W;
+    each_adapter(id, slot, g.slots, [&](int i, uint32_t mask) {
         if (i < 0) return;
-        const uint16_t* a = g.a + ((size_t)i * g.r + min(r0 + row, g.r - 1)) * g.K;
-        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        const uint16_t* a[RR][2];
+#pragma unroll
+        for (int q = 0; q < RR; ++q)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                a[q][h] = g.a + ((size_t)i * g.r + min(r0 + q * 16 + h * 8 + load_row, g.r - 1)) * g.K;
+        f32x4 acc[RR] = {};
+        auto multiply = [&](const u32x4 (&v)[1 + RR][2]) {
+#pragma unroll
+            for (int q = 0; q < 1 + RR; ++q)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    stage[wave][q][(h * 8 + load_row) * 8 + (chunk ^ (load_row & 7))] = v[q][h];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int at = row * 8 + ((h * 4 + quarter) ^ (row & 7));
+                const u32x4 xv = stage[wave][0][at];
+#pragma unroll
+                for (int q = 0; q < RR; ++q) acc[q] = mfma(stage[wave][1 + q][at], xv, acc[q]);
+            }
+        };
         for (int s = s0; s < s1; s += U) {
-            u32x4 av[U], xv[U];
+            u32x4 v[U][1 + RR][2];
 #pragma unroll
             for (int j = 0; j < U; ++j) {
-                const int k = min(s + j, s1 - 1) * 32 + k0;
-                av[j] = *reinterpret_cast<const u32x4_half*>(a + k);
-                xv[j] = *reinterpret_cast<const u32x4_half*>(x + k);
+                const int k = min(s + j, s1 - 1) * 64 + chunk * 8;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    v[j][0][h] = *reinterpret_cast<const u32x4_half*>(x[h] + k);
+#pragma unroll
+                    for (int q = 0; q < RR; ++q) v[j][1 + q][h] = *reinterpret_cast<const u32x4_half*>(a[q][h] + k);
+                }
             }
 #pragma unroll
             for (int j = 0; j < U; ++j)
-                if (s + j < s1) acc = mfma(av[j], xv[j], acc);
+                if (s + j < s1) multiply(v[j]);
         }
-        if (whole * 32 < g.K && wave == W - 1)
-            acc = mfma(load_bf16x8<false>(a, whole * 32 + k0, g.K), load_bf16x8<false>(x, whole * 32 + k0, g.K), acc);
-        part[wave][lane] = acc;
+        if (wave == W - 1 && chunks * 64 < g.K) {
+            u32x4 v[1 + RR][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                v[0][h] = load_bf16x8<false>(x[h], chunks * 64 + chunk * 8, g.K);
+#pragma unroll
+                for (int q = 0; q < RR; ++q) v[1 + q][h] = load_bf16x8<false>(a[q][h], chunks * 64 + chunk * 8, g.K);
+            }
+            multiply(v);
+        }
+#pragma unroll
+        for (int q = 0; q < RR; ++q) part[wave][q][lane] = acc[q];
         __syncthreads();
-        if (wave == 0) {
+        if (wave < RR && (mask >> row & 1)) {
+            f32x4 sum = part[0][wave][lane];
 #pragma unroll
-            for (int w = 1; w < W; ++w) acc += part[w][lane];
+            for (int w = 1; w < W; ++w) sum += part[w][wave][lane];
             const float scale = g.scale != nullptr ? g.scale[i] : 1.0f;
-            const int rank = r0 + (lane >> 4) * 4;
-            if (mine)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    g.u[(size_t)(m0 + row) * g.rp + rank + e] = rank + e < g.r ? acc[e] * scale : 0.0f;
+            store_u(g, m0 + row, r0 + wave * 16 + quarter * 4, sum * scale);
         }
         __syncthreads();
     });
 }
 
-// 16 consecutive values of a row, n of them the row's, to and from fp32.
-template <bool F32>
-__device__ __forceinline__ void load_row16(const void* p, size_t at, int n, float (&v)[16])
+// ---------------------------------------------------------------------------
+// u of one token and 16 rows of A, for few tokens: a wave takes 4 rows of A,
+// all lanes along them, so that few tokens of many adapters read each adapter
+// once and nothing else.
+// ---------------------------------------------------------------------------
+template <bool EVEN>
+__device__ __forceinline__ f32x4 dot_rows(const LoraArgs& g, int i, int64_t m, int r0)
 {
-    if (n >= 16) {
+    constexpr int Q = 4, U = 5;                          // rows, and loads of each in flight
+    const int lane = threadIdx.x & 63;
+    const uint16_t* x = g.x + (size_t)m * g.K;
+    const uint16_t* a[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) a[q] = g.a + ((size_t)i * g.r + min(r0 + q, g.r - 1)) * g.K;
+    float acc[Q] = {};
+    for (int k0 = 0; k0 < g.K; k0 += 512 * U) {
+        u32x4 xv[U], av[Q][U];
+#pragma unroll
+        for (int c = 0; c < U; ++c) {
+            const int k = k0 + (c * 64 + lane) * 8;
+            xv[c] = load_bf16x8<EVEN>(x, k, g.K);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) av[q][c] = load_bf16x8<EVEN>(a[q], k, g.K);
+        }
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+#pragma unroll
+            for (int c = 0; c < U; ++c) acc[q] = dot8(av[q][c], xv[c], acc[q]);
+    }
+    const float scale = g.scale != nullptr ? g.scale[i] : 1.0f;
+    f32x4 u;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) u[q] = wave_sum(acc[q]) * scale;
+    return u;
+}
+
+template <bool EVEN>
+__global__ __launch_bounds__(256) void lora_shrink_few_kernel(LoraArgs g)
+{
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), ranks = (g.r + 15) / 16;
+    const int64_t m = blockIdx.x / ranks;
+    const int i = adapter_of(g, m), r0 = (int)(blockIdx.x % ranks) * 16 + wave * 4;
+    if (i < 0) return;
+    f32x4 u = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (r0 < g.r) u = dot_rows<EVEN>(g, i, m, r0);
+    if ((threadIdx.x & 63) == 0) store_u(g, m, r0, u);
+}
+
+// ---------------------------------------------------------------------------
+// out of up to 64 tokens (token_tiles x 16) and 256 channels, 64 a wave.  u's
+// three parts stand in LDS, rows padded by 16 bytes; they are the first operand
+// and B's rows the second, row q of tile j being channel 4 q + j, so that a lane
+// gets 4 consecutive channels of 4 tokens, and 16 lanes a token's 64: base and
+// out are read and written 128 bytes (bf16) a row.  B's rows stay in registers
+// while the adapter is the same.  RK: steps of 32 ranks.
+// ---------------------------------------------------------------------------
+template <bool F32>
+__device__ __forceinline__ f32x4 load_row4(const void* p, size_t at, int n)
+{
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (n >= 4) {
         if constexpr (F32) {
-            const f32x4_word* q = reinterpret_cast<const f32x4_word*>(static_cast<const float*>(p) + at);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = q[i >> 2][i & 3];
+            v = *reinterpret_cast<const f32x4_word*>(static_cast<const float*>(p) + at);
         } else {
-            const u32x4_half* q = reinterpret_cast<const u32x4_half*>(static_cast<const uint16_t*>(p) + at);
-            const u32x4 d[2] = {q[0], q[1]};
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const uint32_t w = d[i >> 3][(i & 7) >> 1];
-                v[i] = __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
-            }
+            const u32x2 d = *reinterpret_cast<const u32x2_half*>(static_cast<const uint16_t*>(p) + at);
+            v = f32x4{__uint_as_float(d.x << 16), __uint_as_float(d.x & 0xFFFF0000u), __uint_as_float(d.y << 16),
+                      __uint_as_float(d.y & 0xFFFF0000u)};
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = i < n ? load_typed(p, F32 ? kTypeF32 : kTypeBf16, at + i) : 0.0f;
+        for (int i = 0; i < 3; ++i)
+            if (i < n) v[i] = load_typed(p, F32 ? kTypeF32 : kTypeBf16, at + i);
     }
+    return v;
 }
 
 template <bool F32>
-__device__ __forceinline__ void store_row16(void* p, size_t at, int n, const float (&v)[16])
+__device__ __forceinline__ void store_row4(void* p, size_t at, int n, f32x4 v)
 {
-    if (n >= 16) {
+    if (n >= 4) {
         if constexpr (F32) {
-            f32x4_word* q = reinterpret_cast<f32x4_word*>(static_cast<float*>(p) + at);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) q[i] = f32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+            *reinterpret_cast<f32x4_word*>(static_cast<float*>(p) + at) = v;
         } else {
-            u32x4_half* q = reinterpret_cast<u32x4_half*>(static_cast<uint16_t*>(p) + at);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                u32x4 d;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    d[i] = f32_to_bf16_bits(v[8 * h + 2 * i]) | f32_to_bf16_bits(v[8 * h + 2 * i + 1]) << 16;
-                q[h] = d;
-            }
+            const u32x2 d = {f32_to_bf16_bits(v[0]) | f32_to_bf16_bits(v[1]) << 16,
+                             f32_to_bf16_bits(v[2]) | f32_to_bf16_bits(v[3]) << 16};
+            *reinterpret_cast<u32x2_half*>(static_cast<uint16_t*>(p) + at) = d;
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 15; ++i)
+        for (int i = 0; i < 3; ++i)
             if (i < n) {
                 if constexpr (F32) static_cast<float*>(p)[at + i] = v[i];
                 else static_cast<uint16_t*>(p)[at + i] = (uint16_t)f32_to_bf16_bits(v[i]);
@@ -108,63 +203,130 @@ __device__ __forceinline__ void store_row16(void* p, size_t at, int n, const flo
     }
 }
 
-// ---------------------------------------------------------------------------
-// out of TM x 16 tokens and 256 channels, 64 a wave.  The channels are the
-// first operand, row q of tile j being channel 16 (q / 4) + 4 j + q % 4, so that
-// a lane gets 16 consecutive channels of its token over the four tiles.  B's
-// rows stay in registers while the adapter is the same.  RK: steps of 32 ranks.
-// ---------------------------------------------------------------------------
 template <bool F32, int RK, bool EVEN>
 __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs g)
 {
+    extern __shared__ uint32_t us[];                     // [3][token_tiles * 16][rp / 2 + 4]
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int row = lane & 15, k0 = (lane >> 4) * 8;
-    const int64_t tiles = (g.N + 255) / 256;
-    const int slot = (int)(blockIdx.x % g.slots);
-    const int64_t rest = blockIdx.x / g.slots, m_tile = rest / tiles * g.token_tiles * 16;
-    const int64_t n0 = (rest % tiles) * 256 + wave * 64, n = n0 + (lane >> 4) * 16;
+    const int row = lane & 15, quarter = lane >> 4, stride = g.rp / 2 + 4, tokens = g.token_tiles * 16;
+    const int64_t tn = (g.N + 255) / 256, tm = (g.M + tokens - 1) / tokens;
+    const int64_t tile = blockIdx.x % (tm * tn), m_tile = tile / tn * tokens;
+    const int64_t n0 = tile % tn * 256 + wave * 64, n = n0 + row * 4;
+    const int slot = (int)(blockIdx.x / (tm * tn)), left = (int)min((int64_t)4, g.N - n);
+    int id = adapter_of(g, m_tile + row);
+    if (slot > 0) {                                      // (with slots there is one tile of tokens)
+        bool any = false;
+        each_adapter(id, slot, g.slots, [&](int, uint32_t) { any = true; });
+        if (!any) return;
+    }
+    const int quads = g.rp / 4;
+    for (int q = threadIdx.x; q < tokens * quads; q += 256) {
+        const int t = q / quads, c = q - t * quads;
+        const f32x4 u = *reinterpret_cast<const f32x4*>(g.u + (size_t)min(m_tile + t, g.M - 1) * g.rp + 4 * c);
+        const Split3 lo = split_pair(u[0], u[1]), hi = split_pair(u[2], u[3]);
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+            *reinterpret_cast<u32x2*>(us + (p * tokens + t) * stride + 2 * c) = u32x2{lo.v[p], hi.v[p]};
+    }
+    __syncthreads();
     if (n0 >= g.N) return;
-    const int left = (int)min((int64_t)16, g.N - n);     // channels of this lane (may be none)
     u32x4 bv[4][RK];
     int held = -1;
     for (int t = 0; t < g.token_tiles; ++t) {
-        const int64_t m = m_tile + t * 16 + row;
-        if (m_tile + t * 16 >= g.M) return;
-        const int id = adapter_of(g, m);
-        const size_t at = (size_t)min(m, g.M - 1) * g.N + min(n, g.N - 1);
-        float o[16] = {};
-        if (g.base != nullptr) load_row16<F32>(g.base, at, left, o);
-        bool own = false;
-        each_adapter(id, slot, g.slots, [&](int i, bool mine) {
-            own |= mine;
+        const int64_t m0 = m_tile + t * 16;
+        if (m0 >= g.M) return;
+        const int here = id;
+        id = adapter_of(g, m0 + 16 + row);               // the next tile's
+        f32x4 o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            o[e] = g.base != nullptr ? load_row4<F32>(g.base, (size_t)min(m0 + quarter * 4 + e, g.M - 1) * g.N + n, left)
+                                     : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        uint32_t own = 0;
+        each_adapter(here, slot, g.slots, [&](int i, uint32_t mask) {
+            own |= mask;
             if (i < 0) return;
             if (i != held) {
                 held = i;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int64_t c = min(n0 + (row >> 2) * 16 + j * 4 + (row & 3), g.N - 1);
-                    const uint16_t* b = g.b + ((size_t)i * g.N + c) * g.r;
+                    const uint16_t* b = g.b + ((size_t)i * g.N + min(n + j, g.N - 1)) * g.r;
 #pragma unroll
-                    for (int k = 0; k < RK; ++k) bv[j][k] = load_bf16x8<EVEN>(b, 32 * k + k0, g.r);
+                    for (int k = 0; k < RK; ++k) bv[j][k] = load_bf16x8<EVEN>(b, 32 * k + quarter * 8, g.r);
                 }
             }
             f32x4 acc[4] = {};
-            const float* u = g.u + (size_t)min(m, g.M - 1) * g.rp + k0;
 #pragma unroll
             for (int k = 0; k < RK; ++k) {
-                if (k * 32 >= g.rp) break;
-                // (a token of another adapter has its own u here, and drops the result)
-                const Split3 s = split_u(u + 32 * k);
+                if (k * 32 >= g.rp) break;               // (ranks 65 to 96)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int p = 2; p >= 0; --p) {
+                    // (a token of another adapter has its own u here, and drops the result)
+                    const u32x4 uv = *reinterpret_cast<const u32x4*>(us + (p * tokens + t * 16 + row) * stride + 16 * k + quarter * 4);
 #pragma unroll
-                    for (int p = 2; p >= 0; --p) acc[j] = mfma(bv[j][k], s.v[p], acc[j]);
+                    for (int j = 0; j < 4; ++j) acc[j] = mfma(uv, bv[j][k], acc[j]);
+                }
             }
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] += mine ? acc[e >> 2][e & 3] : 0.0f;
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[e][j] += mask >> (quarter * 4 + e) & 1 ? acc[j][e] : 0.0f;
         });
-        if (own && left > 0) store_row16<F32>(g.out, at, left, o);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (own >> (quarter * 4 + e) & 1) store_row4<F32>(g.out, (size_t)(m0 + quarter * 4 + e) * g.N + n, left, o[e]);
     }
+}
+
+// ---------------------------------------------------------------------------
+// out of one token and 256 channels, a thread each: for few tokens, whose lanes
+// a tile of 16 would leave idle.  FUSED: every workgroup computes its token's u
+// itself (A comes from L2 after the first), which saves a launch.
+// ---------------------------------------------------------------------------
+template <bool F32, bool FUSED, bool EVEN>
+__global__ __launch_bounds__(256) void lora_few_kernel(LoraArgs g)
+{
+    __shared__ f32x4 us[kMaxLoraRank / 4];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t m = blockIdx.x % g.M, n = blockIdx.x / g.M * 256 + threadIdx.x;
+    const int i = __builtin_amdgcn_readfirstlane(adapter_of(g, m));
+    const size_t at = (size_t)m * g.N + min(n, g.N - 1);
+    float o = g.base != nullptr ? load_typed(g.base, F32 ? kTypeF32 : kTypeBf16, at) : 0.0f;
+    if (i >= 0) {
+        const uint16_t* b = g.b + ((size_t)i * g.N + min(n, g.N - 1)) * g.r;
+        u32x4 bv[4];                                     // 32 values of the row at a time, the first meanwhile
+#pragma unroll
+        for (int h = 0; h < 4; ++h) bv[h] = load_bf16x8<EVEN>(b, 8 * h, g.r);
+        if constexpr (FUSED) {
+            for (int r0 = wave * 4; r0 < g.rp; r0 += 16) {
+                f32x4 u = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (r0 < g.r) u = dot_rows<true>(g, i, m, r0);   // (K is a multiple of 8)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) u[e] = r0 + e < g.r ? u[e] : 0.0f;
+                if (lane == 0) us[r0 / 4] = u;
+            }
+        } else {
+            for (int q = threadIdx.x; q < g.rp / 4; q += 256) us[q] = reinterpret_cast<const f32x4*>(g.u + m * g.rp)[q];
+        }
+        __syncthreads();
+        float d = 0.0f;
+        for (int j = 0; j < g.rp; j += 32) {
+            if (j > 0)
+#pragma unroll
+                for (int h = 0; h < 4; ++h) bv[h] = load_bf16x8<EVEN>(b, j + 8 * h, g.r);
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t w = bv[h][e >> 1];
+                    d = fmaf(us[(j + 8 * h + e) >> 2][e & 3], __uint_as_float(e & 1 ? w & 0xFFFF0000u : w << 16), d);
+                }
+        }
+        o += d;
+    }
+    if (n >= g.N) return;
+    if constexpr (F32) static_cast<float*>(g.out)[at] = o;
+    else static_cast<uint16_t*>(g.out)[at] = (uint16_t)f32_to_bf16_bits(o);
 }
 
 }  // namespace moe
