@@ -82,10 +82,8 @@ struct LoraArgs {
     void* out;               // [M, N]
     float* u;                // [M, rp], workspace
     int64_t M, N;
-    int K, r, rp, L, out_type;   // rp: r up to a multiple of 32; base is of out's type
-    // by the launcher: workgroups that share a tile's adapters, and tiles of 16
-    // tokens a workgroup takes
-    int slots, token_tiles;
+    int K, r, rp, L, base_type, out_type;   // rp: r up to a multiple of 32
+    int slots;               // by the launcher: workgroups that share a tile's adapters
 };
 
 }  // namespace moe

@@ -49,35 +49,38 @@ constexpr LogprobPlan logprob_plan(int64_t M, int V)
 // ---- adapters ------------------------------------------------------------------
 constexpr int lora_padded(int r) { return (r + 31) / 32 * 32; }   // ranks of a row of u
 
+constexpr int kLoraFewTokens = 64;
+constexpr int kLoraTokenTiles = 4;          // tiles of 16 tokens a workgroup takes where there are many
+constexpr int64_t kLoraFusedWork = 65536;   // values of an adapter's A
+
 struct LoraPlan {
-    bool few, fused, shrink_few;
+    bool few, fused;
     int shrink_slots, expand_slots, token_tiles;
 };
 
-// The adapters of a tile of 16 tokens are dealt to so many workgroups that there
-// are about 1,024 of them (at most 16: a token each).
-constexpr int lora_slots(int64_t tiles)
+// The adapters of a tile of 16 tokens are dealt to so many workgroups (at most
+// 16: a token each) that there is one for every compute unit.
+constexpr int lora_slots(int64_t tiles, int64_t target)
 {
     int slots = 1;
-    while (slots < 16 && tiles * slots < 1024) slots *= 2;
+    while (slots < 16 && tiles * slots < target) slots *= 2;
     return slots;
 }
-
-constexpr int kLoraFewTokens = 64;
-constexpr int64_t kLoraFusedWork = 65536;   // values of an adapter's A
 
 constexpr LoraPlan lora_plan(int64_t M, int64_t N, int64_t K, int r)
 {
     LoraPlan p{};
-    p.few = M <= kLoraFewTokens;
-    p.fused = p.few && K % 8 == 0 && r * K <= kLoraFusedWork && M * ceil_div(N, 256) <= kCus;
-    p.shrink_few = M <= kLoraFewTokens;
-    p.shrink_slots = lora_slots(ceil_div(M, 16) * ceil_div(r, r > 16 ? 32 : 16));
     const int64_t tn = ceil_div(N, 256), tm = ceil_div(M, 16);
-    p.token_tiles = 1;
-    while (p.token_tiles < 4 && ceil_div(tm, 2 * p.token_tiles) * tn >= 2 * kCus) p.token_tiles *= 2;
-    p.expand_slots = p.token_tiles == 1 ? lora_slots(tm * tn) : 1;
+    p.few = M <= kLoraFewTokens;
+    p.fused = p.few && K % 8 == 0 && r * K <= kLoraFusedWork && M * tn <= kCus;
+    p.shrink_slots = lora_slots(tm * ceil_div(r, r > 16 ? 32 : 16), kCus);
+    p.token_tiles = ceil_div(tm, kLoraTokenTiles) * tn >= kCus ? kLoraTokenTiles : 1;
+    p.expand_slots = p.token_tiles == 1 ? lora_slots(tm * tn, 4 * kCus) : 1;
     return p;
 }
+
+// Rows of the int8 product that are kept in fp32 at a time on the way to bf16:
+// 256 MB of them, and 256 at least.
+constexpr int64_t lora_product_rows(int64_t N) { return std::max<int64_t>(256, (1ll << 26) / N / 256 * 256); }
 
 }  // namespace moe

@@ -3,9 +3,7 @@
 // summed exactly in int32, so no order of the sum changes the result.
 #pragma once
 
-#include <type_traits>
-
-#include "lora_common.hpp"
+#include "around_common.hpp"
 
 namespace moe {
 
@@ -78,34 +76,9 @@ __device__ __forceinline__ int32_t dot16(u32x4 a, u32x4 b, int32_t acc)
     return __builtin_amdgcn_sdot4((int)a.w, (int)b.w, acc, false);
 }
 
-// Products alone, or with the tokens' adapters added (LoraArgs, u computed).
-struct NoAdapters {};
-
-template <int L>
-__device__ __forceinline__ float group_sum_f32(float v)
+template <int MT, int U, int L, int R>
+__global__ __launch_bounds__(256) void int8_gemv_kernel(Int8Args g)
 {
-    if constexpr (L == 16) return group_sum<16>(v);
-    else return wave_sum(v);
-}
-
-// sum_j B[i][n, j] u[j] of a token's adapter, by the L lanes of a channel; 0
-// where it has none.
-template <int L>
-__device__ __forceinline__ float gemv_delta(const LoraArgs& a, int t, int64_t n, int li)
-{
-    const int i = adapter_of(a, t);
-    float d = 0.0f;
-    if (i >= 0) {
-        const uint16_t* b = a.b + ((size_t)i * a.N + n) * a.r;
-        for (int j = li; j < a.r; j += L) d = fmaf(a.u[t * a.rp + j], bf16_bits_to_f32(b[j]), d);
-    }
-    return group_sum_f32<L>(d);
-}
-
-template <int MT, int U, int L, int R, typename Adapters = NoAdapters>
-__global__ __launch_bounds__(256) void int8_gemv_kernel(Int8Args g, Adapters ad)
-{
-    constexpr bool LORA = !std::is_same<Adapters, NoAdapters>::value;
     extern __shared__ u32x4 xs[];                        // [token][padded chunk]
     constexpr int CH = 4 * R * (64 / L);                 // channels a workgroup holds
     const int M = (int)g.M, K = g.K, chunks = (K + 15) / 16;
@@ -174,11 +147,8 @@ __global__ __launch_bounds__(256) void int8_gemv_kernel(Int8Args g, Adapters ad)
                     if (t >= M) continue;
                     const int32_t sum = group_sum_i32<L>(acc[r][t]);
                     acc[r][t] = 0;
-                    float delta = 0.0f;
-                    if constexpr (LORA) delta = gemv_delta<L>(ad, t, min(n, g.N - 1), li);
                     if (li == 0 && n < g.N) {
-                        float v = int8_scaled(sum, g.a_scale[t], ws);
-                        if constexpr (LORA) v += delta;
+                        const float v = int8_scaled(sum, g.a_scale[t], ws);
                         if (g.out_type == kTypeF32) static_cast<float*>(g.out)[(size_t)t * g.N + n] = v;
                         else static_cast<uint16_t*>(g.out)[(size_t)t * g.N + n] = (uint16_t)f32_to_bf16_bits(v);
                     }
@@ -251,126 +221,14 @@ __device__ __forceinline__ void wait_steps(int steps)
     }
 }
 
-// The adapters' part of a tile's FM x 16 tokens and FN x 16 channels, as the
-// products above hold them: rows of B are the first operand, so a lane gets
-// channels 4 (l / 16) + 0..3 of tile j and one token.  What it takes from
-// memory (the tokens' adapters and u, B's rows) is asked for as early as it can
-// be: one token tile after another, each would be a round trip or two.
-template <int FM, int FN>
-struct TileAdapters {
-    // B's rows of G adapters together: 16 tokens of a decode batch may have as many
-    static constexpr int G = FM * FN <= 2 ? 4 : FM * FN <= 4 ? 2 : 1;
-    const LoraArgs& a;
-    int64_t m0, n0;
-    int row, k0, ids[FM];
-    f32x4 u[FM][2];                                      // of the first 32 ranks
-    u32x4 bv[G][FN];
-    int held = -1;                                       // the adapter whose first 32 ranks bv[0] has
-
-    __device__ __forceinline__ TileAdapters(const LoraArgs& args, int64_t m, int64_t n) : a(args), m0(m), n0(n)
-    {
-        const int lane = threadIdx.x & 63;
-        row = lane & 15;
-        k0 = (lane >> 4) * 8;
-#pragma unroll
-        for (int i = 0; i < FM; ++i) ids[i] = adapter_of(a, m0 + i * 16 + row);
-        load_u(0, 0, u[0]);
-    }
-
-    __device__ __forceinline__ void load_u(int i, int k, f32x4 (&v)[2]) const
-    {
-        const f32x4* p = reinterpret_cast<const f32x4*>(a.u + (size_t)min(m0 + i * 16 + row, a.M - 1) * a.rp + k0 + k);
-        v[0] = p[0];
-        v[1] = p[1];
-    }
-
-    __device__ __forceinline__ void load_b(int adapter, int k, u32x4 (&v)[FN]) const
-    {
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            const uint16_t* b = a.b + ((size_t)adapter * a.N + min(n0 + j * 16 + row, a.N - 1)) * a.r;
-            v[j] = a.r % 8 == 0 ? load_bf16x8<true>(b, k + k0, a.r) : load_bf16x8<false>(b, k + k0, a.r);
-        }
-    }
-
-    __device__ __forceinline__ void add(const u32x4 (&s)[3], const u32x4 (&v)[FN], f32x4 (&acc)[FN]) const
-    {
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-#pragma unroll
-            for (int p = 2; p >= 0; --p) acc[j] = mfma(v[j], s[p], acc[j]);
-    }
-
-    __device__ __forceinline__ void split(const f32x4 (&v)[2], u32x4 (&s)[3]) const
-    {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const Split3 q = split_pair(v[e >> 1][e & 1 ? 2 : 0], v[e >> 1][e & 1 ? 3 : 1]);
-#pragma unroll
-            for (int p = 0; p < 3; ++p) s[p][e] = q.v[p];
-        }
-    }
-
-    // Token tile i, in turn.
-    __device__ __forceinline__ void delta(int i, f32x4 (&d)[FN])
-    {
-        if (i + 1 < FM) load_u(i + 1, 0, u[i + 1]);
-        uint32_t todo = (uint32_t)__ballot(ids[i] >= 0) & 0xFFFFu;
-        while (todo != 0) {
-            int which[G], n = 0;
-#pragma unroll
-            for (int q = 0; q < G; ++q) {
-                which[q] = -1;
-                if (todo != 0) {
-                    which[q] = __builtin_amdgcn_readlane(ids[i], (int)__builtin_ctz(todo));
-                    todo &= ~(uint32_t)__ballot(ids[i] == which[q]);
-                    ++n;
-                }
-            }
-            f32x4 acc[G][FN] = {};
-            for (int k = 0; k < a.rp; k += 32) {
-                if (k > 0 || held != which[0] || n > 1) {
-#pragma unroll
-                    for (int q = 0; q < G; ++q)
-                        if (q < n) load_b(which[q], k, bv[q]);
-                    held = k == 0 ? which[0] : -1;
-                }
-                u32x4 s[3];
-                if (k == 0) {
-                    split(u[i], s);
-                } else {
-                    f32x4 v[2];
-                    load_u(i, k, v);
-                    split(v, s);
-                }
-#pragma unroll
-                for (int q = 0; q < G; ++q)
-                    if (q < n) add(s, bv[q], acc[q]);
-            }
-#pragma unroll
-            for (int q = 0; q < G; ++q)
-#pragma unroll
-                for (int j = 0; j < FN; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) d[j][e] += q < n && ids[i] == which[q] ? acc[q][j][e] : 0.0f;
-        }
-    }
-};
-
-struct NoTileAdapters {
-    template <typename... T>
-    __device__ __forceinline__ NoTileAdapters(const T&...) {}
-};
-
 template <int N>
 struct Count {
     static constexpr int value = N;
 };
 
-template <int BM, int BN, int WM, int WN, int BK, int S, int EU, bool DIRECT, typename Adapters = NoAdapters>
-__global__ __launch_bounds__(64 * WM * WN, EU) void int8_tile_kernel(Int8Args g, Adapters ad)
+template <int BM, int BN, int WM, int WN, int BK, int S, int EU, bool DIRECT>
+__global__ __launch_bounds__(64 * WM * WN, EU) void int8_tile_kernel(Int8Args g)
 {
-    constexpr bool LORA = !std::is_same<Adapters, NoAdapters>::value;
     constexpr int T = 64 * WM * WN, FM = BM / (16 * WM), FN = BN / (16 * WN), CR = BK / 16;
     constexpr int ROWS = BM + BN, NL = ROWS * CR / T;    // rows in LDS, chunks a thread loads a step
     static_assert(BM % (16 * WM) == 0 && BN % (16 * WN) == 0 && ROWS * CR % T == 0 && BM % (T / CR) == 0, "tile shape");
@@ -408,11 +266,11 @@ __global__ __launch_bounds__(64 * WM * WN, EU) void int8_tile_kernel(Int8Args g,
     auto base = [&](int j) { return j * (T / CR) < BM ? a0 : w0; };
     auto buf = [&](int i) { return lds + i * (ROWS * CR); };
 
-    const int row = lane & 15;
     i32x4 acc[FN][FM] = {};
     struct Frags {
         i32x4 op[FN + FM];                               // operands of 64 codes: channels, then tokens
     };
+    const int row = lane & 15;
     auto read = [&](Frags& f, const u32x4* b, int kk, int i) {
         const int c = (kk * 4 + (lane >> 4)) ^ int8_swizzle<BK>(row);
         const int r = i < FN ? BM + (wn * FN + i) * 16 : (wm * FM + i - FN) * 16;
@@ -534,8 +392,6 @@ __global__ __launch_bounds__(64 * WM * WN, EU) void int8_tile_kernel(Int8Args g,
         }
     }
 
-    typename std::conditional<LORA, TileAdapters<FM, FN>, NoTileAdapters>::type tile_adapters(
-        ad, m0 + wm * FM * 16, n0 + wn * FN * 16);
     // every scale is loaded before the first store: a store may change what a
     // later load reads, for all the compiler knows, so loads among the stores
     // would wait one by one
@@ -549,11 +405,6 @@ __global__ __launch_bounds__(64 * WM * WN, EU) void int8_tile_kernel(Int8Args g,
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         const int64_t m = m0 + (wm * FM + i) * 16 + row;
-        f32x4 delta[LORA ? FN : 1] = {};
-        if constexpr (LORA) {
-            __builtin_amdgcn_sched_barrier(0);           // (one tile's registers at a time)
-            tile_adapters.delta(i, delta);
-        }
         if (m >= g.M) continue;
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
@@ -562,9 +413,6 @@ __global__ __launch_bounds__(64 * WM * WN, EU) void int8_tile_kernel(Int8Args g,
             float o[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) o[r] = int8_scaled(acc[j][i][r], as[i], ws[j][r]);
-            if constexpr (LORA)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) o[r] += delta[j][r];
             const size_t p = (size_t)m * g.N + n;
             const bool all = n + 4 <= g.N;               // a row may start at any address
             if (g.out_type == kTypeF32) {

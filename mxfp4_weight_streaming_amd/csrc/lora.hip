@@ -1,4 +1,5 @@
-// lora.hip -- host launchers of the kernels in lora_kernels.hpp.
+// lora.hip -- host launchers of the kernels in lora_kernels.hpp, alone and behind
+// the int8 product.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -9,72 +10,126 @@
 
 namespace moe {
 
-size_t lora_workspace(int64_t M, int r) { return align256((size_t)M * lora_padded(r) * 4); }
-
 namespace {
 
 constexpr int64_t kMaxThreads = 0xFFFFFFFFll;   // of a launch
 
-template <bool F32, int RK>
-hipError_t expand(LoraArgs a, hipStream_t s)
+int rank_tiles(int r) { return r > 16 ? 2 : 1; }   // of 16, that a workgroup takes
+
+int64_t shrink_grid(const LoraArgs& a, const LoraPlan& p)
+{
+    return ceil_div(a.M, 16) * ceil_div(a.r, 16 * rank_tiles(a.r)) * p.shrink_slots;
+}
+
+int64_t expand_grid(const LoraArgs& a, const LoraPlan& p)
+{
+    return ceil_div(a.M, 16 * p.token_tiles) * ceil_div(a.N, 256) * p.expand_slots;
+}
+
+// Whether the launches are possible: known before the first of them.
+bool fits(const LoraArgs& a)
 {
     const LoraPlan p = lora_plan(a.M, a.N, a.K, a.r);
+    if (p.few) return a.M * ceil_div(a.N, 256) * 256 <= kMaxThreads;
+    return shrink_grid(a, p) * 512 <= kMaxThreads && expand_grid(a, p) * 256 <= kMaxThreads;
+}
+
+template <bool BASE32, bool F32, int RK, bool EVEN>
+hipError_t expand_tiles(LoraArgs a, const LoraPlan& p, hipStream_t s)
+{
     a.slots = p.expand_slots;
-    a.token_tiles = p.token_tiles;
-    const int64_t grid = ceil_div(a.M, 16 * p.token_tiles) * ceil_div(a.N, 256) * a.slots;
-    if (grid * 256 > kMaxThreads) return hipErrorInvalidConfiguration;
-    const auto kernel = a.r % 8 == 0 ? lora_expand_kernel<F32, RK, true> : lora_expand_kernel<F32, RK, false>;
+    const int64_t grid = expand_grid(a, p);
+    const auto kernel = p.token_tiles == 1 ? lora_expand_kernel<BASE32, F32, RK, EVEN, 1>
+                                           : lora_expand_kernel<BASE32, F32, RK, EVEN, kLoraTokenTiles>;
     const uint32_t lds = 3 * 16 * p.token_tiles * (a.rp / 2 + 4) * 4;
     hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(256), lds, s, a);
     return hipGetLastError();
 }
 
-template <bool F32>
-hipError_t expand_ranks(const LoraArgs& a, hipStream_t s)
+template <bool BASE32, bool F32>
+hipError_t expand(const LoraArgs& a, const LoraPlan& p, hipStream_t s)
 {
-    return a.r <= 32 ? expand<F32, 1>(a, s) : a.r <= 64 ? expand<F32, 2>(a, s) : expand<F32, 4>(a, s);
+    if (a.r % 8 != 0) return expand_tiles<BASE32, F32, 4, false>(a, p, s);
+    if (a.r <= 32) return expand_tiles<BASE32, F32, 1, true>(a, p, s);
+    return a.r <= 64 ? expand_tiles<BASE32, F32, 2, true>(a, p, s) : expand_tiles<BASE32, F32, 4, true>(a, p, s);
 }
 
-}  // namespace
-
-namespace {
-
-template <bool F32, bool FUSED>
+template <bool BASE32, bool F32, bool FUSED>
 hipError_t few(const LoraArgs& a, hipStream_t s)
 {
-    const auto kernel = a.r % 8 == 0 ? lora_few_kernel<F32, FUSED, true> : lora_few_kernel<F32, FUSED, false>;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)(a.M * ceil_div(a.N, 256))), dim3(256), 0, s, a);
+    const int64_t grid = a.M * ceil_div(a.N, 256);
+    const auto kernel = a.r % 8 == 0 ? lora_few_kernel<BASE32, F32, FUSED, true> : lora_few_kernel<BASE32, F32, FUSED, false>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
-}  // namespace
-
-hipError_t launch_lora_shrink(LoraArgs a, hipStream_t s)
+hipError_t shrink(LoraArgs a, const LoraPlan& p, hipStream_t s)
 {
-    const LoraPlan p = lora_plan(a.M, a.N, a.K, a.r);
-    if (p.shrink_few) {
+    if (p.few) {
         const auto kernel = a.K % 8 == 0 ? lora_shrink_few_kernel<true> : lora_shrink_few_kernel<false>;
         hipLaunchKernelGGL(kernel, dim3((unsigned)(a.M * ceil_div(a.r, 16))), dim3(256), 0, s, a);
         return hipGetLastError();
     }
     a.slots = p.shrink_slots;
-    const int rr = a.r > 16 ? 2 : 1;
-    const int64_t grid = ceil_div(a.M, 16) * ceil_div(a.r, 16 * rr) * a.slots;
-    if (grid * 512 > kMaxThreads) return hipErrorInvalidConfiguration;
-    const auto kernel = rr == 2 ? lora_shrink_kernel<2> : lora_shrink_kernel<1>;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(512), 0, s, a);
+    const int64_t grid = shrink_grid(a, p);
+    hipLaunchKernelGGL((rank_tiles(a.r) == 2 ? lora_shrink_kernel<2> : lora_shrink_kernel<1>), dim3((unsigned)grid), dim3(512), 0, s, a);
     return hipGetLastError();
+}
+
+template <bool BASE32, bool F32>
+hipError_t add(const LoraArgs& a, hipStream_t s)
+{
+    const LoraPlan p = lora_plan(a.M, a.N, a.K, a.r);
+    if (p.fused) return few<BASE32, F32, true>(a, s);
+    const hipError_t e = shrink(a, p, s);
+    if (e != hipSuccess) return e;
+    return p.few ? few<BASE32, F32, false>(a, s) : expand<BASE32, F32>(a, p, s);
+}
+
+size_t u_bytes(int64_t M, int r) { return align256((size_t)M * lora_padded(r) * 4); }
+
+}  // namespace
+
+size_t lora_workspace(int64_t M, int64_t N, int r)
+{
+    return u_bytes(M, r) + (size_t)std::min<int64_t>(M, lora_product_rows(N)) * N * 4;
 }
 
 hipError_t launch_lora_add(const LoraArgs& a, hipStream_t s)
 {
-    const LoraPlan p = lora_plan(a.M, a.N, a.K, a.r);
+    if (!fits(a)) return hipErrorInvalidConfiguration;
+    return a.out_type == kTypeF32 ? add<true, true>(a, s) : add<false, false>(a, s);
+}
+
+// The product in fp32 first, into out where that is fp32 and else into the
+// workspace, 256 MB at a time; then the adapters on top of it.
+hipError_t launch_int8_linear_lora(const Int8Args& p, const LoraArgs& a, hipStream_t s)
+{
+    if (!fits(a)) return hipErrorInvalidConfiguration;   // (what fits here is fewer tiles than a product may have)
     const bool f32 = a.out_type == kTypeF32;
-    if (p.few && p.fused) return f32 ? few<true, true>(a, s) : few<false, true>(a, s);
-    const hipError_t e = launch_lora_shrink(a, s);
-    if (e != hipSuccess) return e;
-    if (p.few) return f32 ? few<true, false>(a, s) : few<false, false>(a, s);
-    return f32 ? expand_ranks<true>(a, s) : expand_ranks<false>(a, s);
+    const int64_t step = f32 ? a.M : lora_product_rows(a.N);
+    for (int64_t m = 0; m < a.M; m += step) {
+        Int8Args g = p;
+        LoraArgs l = a;
+        g.M = l.M = std::min(step, a.M - m);
+        g.a += (size_t)m * p.K;
+        g.a_scale += m;
+        l.x += (size_t)m * a.K;
+        l.ids += m;
+        if (f32) {
+            l.base = l.out;
+        } else {
+            g.out = reinterpret_cast<uint8_t*>(a.u) + u_bytes(a.M, a.r);
+            l.base = g.out;
+            l.out = static_cast<uint16_t*>(a.out) + (size_t)m * a.N;
+        }
+        g.out_type = kTypeF32;
+        hipError_t e = launch_int8_linear(g, s);
+        if (e != hipSuccess) return e;
+        e = f32 ? add<true, true>(l, s) : add<true, false>(l, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace moe

@@ -1,10 +1,110 @@
-// lora_kernels.hpp -- the adapters' two products: u of each token, and B u added
-// to a projection's output (gfx950; lora_common.hpp says how tokens are taken).
+// lora_kernels.hpp -- low-rank adapters of many requests (gfx950): token m has
+// adapter i = ids[m], and
+//   u[m] = scale[i] A[i] x[m]             (r values, fp32; kept with zeros behind
+//                                          them up to a multiple of 32, rp)
+//   out[m] = round(base[m] + B[i] u[m])   base alone where i is no adapter
+//
+// Tokens are taken as they stand, 16 at a time, which is a matrix instruction's
+// width: a request's tokens follow one another, so 16 of them have few adapters.
+// Each adapter among them is multiplied by all 16, and each token takes its own
+// adapter's result, so nothing of another adapter, infinities and NaN included,
+// reaches it.  Where tiles are few, their adapters are dealt to several
+// workgroups (slots).
+//
+// v_mfma_f32_16x16x32_bf16: lane l gives row l % 16, values 8 (l / 16).. of both
+// operands, and gets rows 4 (l / 16) + 0..3 of the first and row l % 16 of the
+// second, the token.  u goes into the second product as three bf16 numbers that
+// add up to the fp32 one (8 bits each), so it is not rounded.
 #pragma once
 
-#include "lora_common.hpp"
+#include "around_common.hpp"
 
 namespace moe {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_half __attribute__((aligned(2)));    // at any bf16
+typedef u32x2 u32x2_half __attribute__((aligned(2)));
+typedef f32x4 f32x4_word __attribute__((aligned(4)));    // at any fp32
+typedef u32x4 u32x4_word __attribute__((aligned(4)));
+
+// The adapter of token m, or -1; -2 for what is no token.
+__device__ __forceinline__ int adapter_of(const LoraArgs& g, int64_t m)
+{
+    if (m >= g.M) return -2;
+    const int i = g.ids[m];
+    return i >= 0 && i < g.L ? i : -1;
+}
+
+// Calls f(adapter, mask of the tokens that have it) for each adapter among the
+// wave's 16 tokens (-1, none, too) that falls to `slot` of `slots` (a power of
+// two).
+template <typename F>
+__device__ __forceinline__ void each_adapter(int id, int slot, int slots, F f)
+{
+    uint32_t todo = (uint32_t)__ballot(id >= -1) & 0xFFFFu;
+    for (int d = 0; todo != 0; ++d) {
+        const int i = __builtin_amdgcn_readlane(id, (int)__builtin_ctz(todo));
+        const uint32_t mask = (uint32_t)__ballot(id == i) & 0xFFFFu;
+        todo &= ~mask;
+        if ((d & (slots - 1)) == slot) f(i, mask);
+    }
+}
+
+// Values k .. k + 7 of a row of n, zeros behind it.  EVEN: n is a multiple of 8,
+// so they are all there or none is, and the load needs no branch.
+template <bool EVEN>
+__device__ __forceinline__ u32x4 load_bf16x8(const uint16_t* row, int k, int n)
+{
+    if constexpr (EVEN) {
+        const u32x4 v = *reinterpret_cast<const u32x4_half*>(row + (k < n ? k : 0));
+        return k < n ? v : u32x4{0, 0, 0, 0};
+    }
+    const uint16_t* p = row + k;
+    if (k + 8 <= n) return *reinterpret_cast<const u32x4_half*>(p);
+    uint32_t d[4] = {0, 0, 0, 0};
+    if (k < n)
+#pragma unroll
+        for (int i = 0; i < 7; ++i) {                    // (all asked for at once)
+            const uint32_t v = p[min(i, n - 1 - k)];
+            d[i >> 1] |= (k + i < n ? v : 0) << (16 * (i & 1));
+        }
+    return u32x4{d[0], d[1], d[2], d[3]};
+}
+
+// acc + the sum of 8 products, one after another in fp32.
+__device__ __forceinline__ float dot8(u32x4 a, u32x4 b, float acc)
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        acc = fmaf(__uint_as_float(a[e] << 16), __uint_as_float(b[e] << 16), acc);
+        acc = fmaf(__uint_as_float(a[e] & 0xFFFF0000u), __uint_as_float(b[e] & 0xFFFF0000u), acc);
+    }
+    return acc;
+}
+
+__device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// Two fp32 values as three pairs of bf16 that add up to them.
+struct Split3 {
+    uint32_t v[3];
+};
+
+__device__ __forceinline__ Split3 split_pair(float a, float b)
+{
+    Split3 s;
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+        const uint32_t lo = f32_to_bf16_bits(a), hi = f32_to_bf16_bits(b);
+        s.v[p] = lo | hi << 16;
+        a -= bf16_bits_to_f32(lo);
+        b -= bf16_bits_to_f32(hi);
+    }
+    return s;
+}
 
 // u of ranks k .. k + 3 of a token, zeros behind r; the 16 behind a last tile
 // that ends in the middle of 32 are cleared with it.
@@ -163,31 +263,47 @@ __global__ __launch_bounds__(256) void lora_shrink_few_kernel(LoraArgs g)
 // while the adapter is the same.  RK: steps of 32 ranks.
 // ---------------------------------------------------------------------------
 template <bool F32>
-__device__ __forceinline__ f32x4 load_row4(const void* p, size_t at, int n)
+struct Row4 {
+    uint32_t d[F32 ? 4 : 2];
+    __device__ __forceinline__ float get(int i) const
+    {
+        if constexpr (F32) return __uint_as_float(d[i]);
+        return __uint_as_float(i & 1 ? d[i >> 1] & 0xFFFF0000u : d[i >> 1] << 16);
+    }
+};
+
+// 4 consecutive values from `at`, of which n (may be 0 or less) are the row's.
+template <bool F32>
+__device__ __forceinline__ Row4<F32> load_row4(const void* p, size_t at, int n)
 {
-    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    Row4<F32> v = {};
     if (n >= 4) {
         if constexpr (F32) {
-            v = *reinterpret_cast<const f32x4_word*>(static_cast<const float*>(p) + at);
+            const u32x4 d = *reinterpret_cast<const u32x4_word*>(static_cast<const float*>(p) + at);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v.d[i] = d[i];
         } else {
             const u32x2 d = *reinterpret_cast<const u32x2_half*>(static_cast<const uint16_t*>(p) + at);
-            v = f32x4{__uint_as_float(d.x << 16), __uint_as_float(d.x & 0xFFFF0000u), __uint_as_float(d.y << 16),
-                      __uint_as_float(d.y & 0xFFFF0000u)};
+            v.d[0] = d.x;
+            v.d[1] = d.y;
         }
     } else {
 #pragma unroll
         for (int i = 0; i < 3; ++i)
-            if (i < n) v[i] = load_typed(p, F32 ? kTypeF32 : kTypeBf16, at + i);
+            if (i < n) {
+                if constexpr (F32) v.d[i] = static_cast<const uint32_t*>(p)[at + i];
+                else v.d[i >> 1] |= (uint32_t) static_cast<const uint16_t*>(p)[at + i] << (16 * (i & 1));
+            }
     }
     return v;
 }
 
 template <bool F32>
-__device__ __forceinline__ void store_row4(void* p, size_t at, int n, f32x4 v)
+__device__ __forceinline__ void store_row4(void* p, size_t at, int n, const float (&v)[4])
 {
     if (n >= 4) {
         if constexpr (F32) {
-            *reinterpret_cast<f32x4_word*>(static_cast<float*>(p) + at) = v;
+            *reinterpret_cast<f32x4_word*>(static_cast<float*>(p) + at) = f32x4{v[0], v[1], v[2], v[3]};
         } else {
             const u32x2 d = {f32_to_bf16_bits(v[0]) | f32_to_bf16_bits(v[1]) << 16,
                              f32_to_bf16_bits(v[2]) | f32_to_bf16_bits(v[3]) << 16};
@@ -203,21 +319,40 @@ __device__ __forceinline__ void store_row4(void* p, size_t at, int n, f32x4 v)
     }
 }
 
-template <bool F32, int RK, bool EVEN>
+template <bool BASE32, bool F32, int RK, bool EVEN, int TT>
 __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs g)
 {
-    extern __shared__ uint32_t us[];                     // [3][token_tiles * 16][rp / 2 + 4]
+    constexpr int tokens = 16 * TT;
+    extern __shared__ uint32_t us[];                     // [3][tokens][rp / 2 + 4]
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int row = lane & 15, quarter = lane >> 4, stride = g.rp / 2 + 4, tokens = g.token_tiles * 16;
+    const int row = lane & 15, quarter = lane >> 4, stride = g.rp / 2 + 4;
     const int64_t tn = (g.N + 255) / 256, tm = (g.M + tokens - 1) / tokens;
     const int64_t tile = blockIdx.x % (tm * tn), m_tile = tile / tn * tokens;
     const int64_t n0 = tile % tn * 256 + wave * 64, n = n0 + row * 4;
-    const int slot = (int)(blockIdx.x / (tm * tn)), left = (int)min((int64_t)4, g.N - n);
-    int id = adapter_of(g, m_tile + row);
-    if (slot > 0) {                                      // (with slots there is one tile of tokens)
+    const int slot = (int)(blockIdx.x / (tm * tn)), left = (int)max((int64_t)0, min((int64_t)4, g.N - n));
+    int id[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) id[t] = adapter_of(g, m_tile + t * 16 + row);
+    // everything that a tile reads is asked for before its first store, which
+    // could change it for all the compiler knows (base may be out)
+    Row4<BASE32> base[TT][4];
+    auto load_base = [&] {
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                base[t][e] = {};
+                if (g.base != nullptr)
+                    base[t][e] = load_row4<BASE32>(g.base, (size_t)min(m_tile + t * 16 + quarter * 4 + e, g.M - 1) * g.N + n, left);
+            }
+    };
+    if (slot == 0) {
+        load_base();
+    } else {                                             // (slots are for one tile of tokens)
         bool any = false;
-        each_adapter(id, slot, g.slots, [&](int, uint32_t) { any = true; });
+        each_adapter(id[0], slot, g.slots, [&](int, uint32_t) { any = true; });
         if (!any) return;
+        load_base();
     }
     const int quads = g.rp / 4;
     for (int q = threadIdx.x; q < tokens * quads; q += 256) {
@@ -228,22 +363,19 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs g)
         for (int p = 0; p < 3; ++p)
             *reinterpret_cast<u32x2*>(us + (p * tokens + t) * stride + 2 * c) = u32x2{lo.v[p], hi.v[p]};
     }
-    __syncthreads();
-    if (n0 >= g.N) return;
+    lds_barrier();
     u32x4 bv[4][RK];
     int held = -1;
-    for (int t = 0; t < g.token_tiles; ++t) {
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
         const int64_t m0 = m_tile + t * 16;
-        if (m0 >= g.M) return;
-        const int here = id;
-        id = adapter_of(g, m0 + 16 + row);               // the next tile's
-        f32x4 o[4];
+        float o[4][4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            o[e] = g.base != nullptr ? load_row4<F32>(g.base, (size_t)min(m0 + quarter * 4 + e, g.M - 1) * g.N + n, left)
-                                     : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[e][j] = base[t][e].get(j);
         uint32_t own = 0;
-        each_adapter(here, slot, g.slots, [&](int i, uint32_t mask) {
+        each_adapter(id[t], slot, g.slots, [&](int i, uint32_t mask) {
             own |= mask;
             if (i < 0) return;
             if (i != held) {
@@ -283,7 +415,7 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs g)
 // a tile of 16 would leave idle.  FUSED: every workgroup computes its token's u
 // itself (A comes from L2 after the first), which saves a launch.
 // ---------------------------------------------------------------------------
-template <bool F32, bool FUSED, bool EVEN>
+template <bool BASE32, bool F32, bool FUSED, bool EVEN>
 __global__ __launch_bounds__(256) void lora_few_kernel(LoraArgs g)
 {
     __shared__ f32x4 us[kMaxLoraRank / 4];
@@ -291,7 +423,7 @@ __global__ __launch_bounds__(256) void lora_few_kernel(LoraArgs g)
     const int64_t m = blockIdx.x % g.M, n = blockIdx.x / g.M * 256 + threadIdx.x;
     const int i = __builtin_amdgcn_readfirstlane(adapter_of(g, m));
     const size_t at = (size_t)m * g.N + min(n, g.N - 1);
-    float o = g.base != nullptr ? load_typed(g.base, F32 ? kTypeF32 : kTypeBf16, at) : 0.0f;
+    float o = g.base != nullptr ? load_typed(g.base, BASE32 ? kTypeF32 : kTypeBf16, at) : 0.0f;
     if (i >= 0) {
         const uint16_t* b = g.b + ((size_t)i * g.N + min(n, g.N - 1)) * g.r;
         u32x4 bv[4];                                     // 32 values of the row at a time, the first meanwhile
