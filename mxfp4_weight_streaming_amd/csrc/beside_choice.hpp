@@ -49,13 +49,15 @@ constexpr LogprobPlan logprob_plan(int64_t M, int V)
 // ---- adapters ------------------------------------------------------------------
 constexpr int lora_padded(int r) { return (r + 31) / 32 * 32; }   // ranks of a row of u
 
-constexpr int kLoraFewTokens = 64;
-constexpr int kLoraTokenTiles = 4;          // tiles of 16 tokens a workgroup takes where there are many
+// Few tokens: a thread a channel, a wave a row of A (256 tokens of rank 16, all
+// of adapters of their own 7.7 us against 15.8 on the matrix cores, of two
+// requests 7.6 against 8.6; rank 64 23 against 29, and 19 against 10).
+constexpr int64_t kLoraFewValues = 8192;    // tokens times their padded rank
 constexpr int64_t kLoraFusedWork = 65536;   // values of an adapter's A
 
 struct LoraPlan {
     bool few, fused;
-    int shrink_slots, expand_slots, token_tiles;
+    int shrink_slots, expand_slots;
 };
 
 // The adapters of a tile of 16 tokens are dealt to so many workgroups (at most
@@ -71,11 +73,10 @@ constexpr LoraPlan lora_plan(int64_t M, int64_t N, int64_t K, int r)
 {
     LoraPlan p{};
     const int64_t tn = ceil_div(N, 256), tm = ceil_div(M, 16);
-    p.few = M <= kLoraFewTokens;
+    p.few = M * lora_padded(r) <= kLoraFewValues;
     p.fused = p.few && K % 8 == 0 && r * K <= kLoraFusedWork && M * tn <= kCus;
     p.shrink_slots = lora_slots(tm * ceil_div(r, r > 16 ? 32 : 16), kCus);
-    p.token_tiles = ceil_div(tm, kLoraTokenTiles) * tn >= kCus ? kLoraTokenTiles : 1;
-    p.expand_slots = p.token_tiles == 1 ? lora_slots(tm * tn, 4 * kCus) : 1;
+    p.expand_slots = lora_slots(tm * tn, 4 * kCus);
     return p;
 }
 

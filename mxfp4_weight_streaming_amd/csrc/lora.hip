@@ -23,7 +23,7 @@ int64_t shrink_grid(const LoraArgs& a, const LoraPlan& p)
 
 int64_t expand_grid(const LoraArgs& a, const LoraPlan& p)
 {
-    return ceil_div(a.M, 16 * p.token_tiles) * ceil_div(a.N, 256) * p.expand_slots;
+    return ceil_div(a.M, 16) * ceil_div(a.N, 256) * p.expand_slots;
 }
 
 // Whether the launches are possible: known before the first of them.
@@ -39,9 +39,8 @@ hipError_t expand_tiles(LoraArgs a, const LoraPlan& p, hipStream_t s)
 {
     a.slots = p.expand_slots;
     const int64_t grid = expand_grid(a, p);
-    const auto kernel = p.token_tiles == 1 ? lora_expand_kernel<BASE32, F32, RK, EVEN, 1>
-                                           : lora_expand_kernel<BASE32, F32, RK, EVEN, kLoraTokenTiles>;
-    const uint32_t lds = 3 * 16 * p.token_tiles * (a.rp / 2 + 4) * 4;
+    const auto kernel = lora_expand_kernel<BASE32, F32, RK, EVEN>;
+    const uint32_t lds = 3 * 16 * (a.rp / 2 + 4) * 4;
     hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(256), lds, s, a);
     return hipGetLastError();
 }

@@ -255,12 +255,12 @@ __global__ __launch_bounds__(256) void lora_shrink_few_kernel(LoraArgs g)
 }
 
 // ---------------------------------------------------------------------------
-// out of up to 64 tokens (token_tiles x 16) and 256 channels, 64 a wave.  u's
+// out of 16 tokens and 256 channels, 64 a wave.  u's
 // three parts stand in LDS, rows padded by 16 bytes; they are the first operand
 // and B's rows the second, row q of tile j being channel 4 q + j, so that a lane
 // gets 4 consecutive channels of 4 tokens, and 16 lanes a token's 64: base and
-// out are read and written 128 bytes (bf16) a row.  B's rows stay in registers
-// while the adapter is the same.  RK: steps of 32 ranks.
+// out are read and written 128 bytes (bf16) a row.  (Two or four tiles of tokens in
+// turn, B's rows kept, were no faster.)  RK: steps of 32 ranks.
 // ---------------------------------------------------------------------------
 template <bool F32>
 struct Row4 {
@@ -319,95 +319,88 @@ __device__ __forceinline__ void store_row4(void* p, size_t at, int n, const floa
     }
 }
 
-template <bool BASE32, bool F32, int RK, bool EVEN, int TT>
+template <bool BASE32, bool F32, int RK, bool EVEN>
 __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs g)
 {
-    constexpr int tokens = 16 * TT;
-    extern __shared__ uint32_t us[];                     // [3][tokens][rp / 2 + 4]
+    extern __shared__ uint32_t us[];                     // [3][16][rp / 2 + 4]
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = lane & 15, quarter = lane >> 4, stride = g.rp / 2 + 4;
-    const int64_t tn = (g.N + 255) / 256, tm = (g.M + tokens - 1) / tokens;
-    const int64_t tile = blockIdx.x % (tm * tn), m_tile = tile / tn * tokens;
+    const int64_t tn = (g.N + 255) / 256, tm = (g.M + 15) / 16;
+    const int64_t tile = blockIdx.x % (tm * tn), m0 = tile / tn * 16;
     const int64_t n0 = tile % tn * 256 + wave * 64, n = n0 + row * 4;
     const int slot = (int)(blockIdx.x / (tm * tn)), left = (int)max((int64_t)0, min((int64_t)4, g.N - n));
-    int id[TT];
-#pragma unroll
-    for (int t = 0; t < TT; ++t) id[t] = adapter_of(g, m_tile + t * 16 + row);
-    // everything that a tile reads is asked for before its first store, which
-    // could change it for all the compiler knows (base may be out)
-    Row4<BASE32> base[TT][4];
-    auto load_base = [&] {
-#pragma unroll
-        for (int t = 0; t < TT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                base[t][e] = {};
-                if (g.base != nullptr)
-                    base[t][e] = load_row4<BASE32>(g.base, (size_t)min(m_tile + t * 16 + quarter * 4 + e, g.M - 1) * g.N + n, left);
-            }
-    };
-    if (slot == 0) {
-        load_base();
-    } else {                                             // (slots are for one tile of tokens)
+    const int id = adapter_of(g, m0 + row);
+    if (slot > 0) {
         bool any = false;
-        each_adapter(id[0], slot, g.slots, [&](int, uint32_t) { any = true; });
+        each_adapter(id, slot, g.slots, [&](int, uint32_t) { any = true; });
         if (!any) return;
-        load_base();
     }
+    // What a tile reads is asked for at once: u, base (all of it before the first
+    // store, which could change it for all the compiler knows, base may be out),
+    // and B's rows for the first token's adapter.
+    constexpr int UQ = (RK + 1) / 2;                     // quads of u a thread
     const int quads = g.rp / 4;
-    for (int q = threadIdx.x; q < tokens * quads; q += 256) {
-        const int t = q / quads, c = q - t * quads;
-        const f32x4 u = *reinterpret_cast<const f32x4*>(g.u + (size_t)min(m_tile + t, g.M - 1) * g.rp + 4 * c);
-        const Split3 lo = split_pair(u[0], u[1]), hi = split_pair(u[2], u[3]);
+    f32x4 uq[UQ];
 #pragma unroll
-        for (int p = 0; p < 3; ++p)
-            *reinterpret_cast<u32x2*>(us + (p * tokens + t) * stride + 2 * c) = u32x2{lo.v[p], hi.v[p]};
+    for (int i = 0; i < UQ; ++i) {
+        const int q = min((int)threadIdx.x + 256 * i, 16 * quads - 1), t = q / quads;
+        uq[i] = *reinterpret_cast<const f32x4*>(g.u + (size_t)min(m0 + t, g.M - 1) * g.rp + 4 * (q - t * quads));
+    }
+    Row4<BASE32> base[4] = {};
+    if (g.base != nullptr)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            base[e] = load_row4<BASE32>(g.base, (size_t)min(m0 + quarter * 4 + e, g.M - 1) * g.N + n, left);
+    u32x4 bv[4][RK];
+    auto load_b = [&](int i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint16_t* b = g.b + ((size_t)i * g.N + min(n + j, g.N - 1)) * g.r;
+#pragma unroll
+            for (int k = 0; k < RK; ++k) bv[j][k] = load_bf16x8<EVEN>(b, 32 * k + quarter * 8, g.r);
+        }
+    };
+    int held = slot == 0 ? __builtin_amdgcn_readlane(id, 0) : -1;
+    if (held >= 0) load_b(held);
+#pragma unroll
+    for (int i = 0; i < UQ; ++i) {
+        const int q = threadIdx.x + 256 * i, t = q / quads, c = q - t * quads;
+        if (q >= 16 * quads) break;
+        const Split3 lo = split_pair(uq[i][0], uq[i][1]), hi = split_pair(uq[i][2], uq[i][3]);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) *reinterpret_cast<u32x2*>(us + (p * 16 + t) * stride + 2 * c) = u32x2{lo.v[p], hi.v[p]};
     }
     lds_barrier();
-    u32x4 bv[4][RK];
-    int held = -1;
+    float o[4][4];
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-        const int64_t m0 = m_tile + t * 16;
-        float o[4][4];
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[e][j] = base[e].get(j);
+    uint32_t own = 0;
+    each_adapter(id, slot, g.slots, [&](int i, uint32_t mask) {
+        own |= mask;
+        if (i < 0) return;
+        if (i != held) load_b(held = i);
+        f32x4 acc[4] = {};
+#pragma unroll
+        for (int k = 0; k < RK; ++k) {
+            if (k * 32 >= g.rp) break;                   // (ranks 65 to 96)
+#pragma unroll
+            for (int p = 2; p >= 0; --p) {
+                // (a token of another adapter has its own u here, and drops the result)
+                const u32x4 uv = *reinterpret_cast<const u32x4*>(us + (p * 16 + row) * stride + 16 * k + quarter * 4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[j] = mfma(uv, bv[j][k], acc[j]);
+            }
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o[e][j] = base[t][e].get(j);
-        uint32_t own = 0;
-        each_adapter(id[t], slot, g.slots, [&](int i, uint32_t mask) {
-            own |= mask;
-            if (i < 0) return;
-            if (i != held) {
-                held = i;
+            for (int j = 0; j < 4; ++j) o[e][j] += mask >> (quarter * 4 + e) & 1 ? acc[j][e] : 0.0f;
+    });
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint16_t* b = g.b + ((size_t)i * g.N + min(n + j, g.N - 1)) * g.r;
-#pragma unroll
-                    for (int k = 0; k < RK; ++k) bv[j][k] = load_bf16x8<EVEN>(b, 32 * k + quarter * 8, g.r);
-                }
-            }
-            f32x4 acc[4] = {};
-#pragma unroll
-            for (int k = 0; k < RK; ++k) {
-                if (k * 32 >= g.rp) break;               // (ranks 65 to 96)
-#pragma unroll
-                for (int p = 2; p >= 0; --p) {
-                    // (a token of another adapter has its own u here, and drops the result)
-                    const u32x4 uv = *reinterpret_cast<const u32x4*>(us + (p * tokens + t * 16 + row) * stride + 16 * k + quarter * 4);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[j] = mfma(uv, bv[j][k], acc[j]);
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) o[e][j] += mask >> (quarter * 4 + e) & 1 ? acc[j][e] : 0.0f;
-        });
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (own >> (quarter * 4 + e) & 1) store_row4<F32>(g.out, (size_t)(m0 + quarter * 4 + e) * g.N + n, left, o[e]);
-    }
+    for (int e = 0; e < 4; ++e)
+        if (own >> (quarter * 4 + e) & 1) store_row4<F32>(g.out, (size_t)(m0 + quarter * 4 + e) * g.N + n, left, o[e]);
 }
 
 // ---------------------------------------------------------------------------
