@@ -49,10 +49,11 @@ constexpr LogprobPlan logprob_plan(int64_t M, int V)
 // ---- adapters ------------------------------------------------------------------
 constexpr int lora_padded(int r) { return (r + 31) / 32 * 32; }   // ranks of a row of u
 
-// Few tokens: a thread a channel, a wave a row of A (256 tokens of rank 16, all
-// of adapters of their own 7.7 us against 15.8 on the matrix cores, of two
-// requests 7.6 against 8.6; rank 64 23 against 29, and 19 against 10).
-constexpr int64_t kLoraFewValues = 8192;    // tokens times their padded rank
+// Few tokens: each reads its adapter by itself.  256 tokens of rank 64, each of
+// another adapter: 15.9 us against 29.2 on the matrix cores, where a tile of 16
+// tokens takes its adapters in turn; of two requests 12.7 against 10.0.  512 of
+// rank 16: 10.4 against 25.3, and 10.3 against 9.5.
+constexpr int64_t kLoraFewValues = 16384;   // tokens times their padded rank
 constexpr int64_t kLoraFusedWork = 65536;   // values of an adapter's A
 
 struct LoraPlan {

@@ -51,24 +51,30 @@ __device__ __forceinline__ void each_adapter(int id, int slot, int slots, F f)
     }
 }
 
-// Values k .. k + 7 of a row of n, zeros behind it.  EVEN: n is a multiple of 8,
-// so they are all there or none is, and the load needs no branch.
+// Values k .. k + 7 of a row of n.  EVEN: n is a multiple of 8, so they are all
+// there or none is, and what is read where none is (the row's first) is put to 0
+// by the caller, after it has asked for everything (a zero put in here would be
+// waited for at once).  Else zeros stand behind the row; a part of it comes from
+// its last 8, shifted down, and only rows shorter than 8 are read value by value.
 template <bool EVEN>
 __device__ __forceinline__ u32x4 load_bf16x8(const uint16_t* row, int k, int n)
 {
-    if constexpr (EVEN) {
-        const u32x4 v = *reinterpret_cast<const u32x4_half*>(row + (k < n ? k : 0));
-        return k < n ? v : u32x4{0, 0, 0, 0};
+    if constexpr (EVEN) return *reinterpret_cast<const u32x4_half*>(row + (k < n ? k : 0));
+    if (n >= 8) {
+        const int at = min(k, n - 8), by = k - at;       // values to drop
+        const u32x4 v = *reinterpret_cast<const u32x4_half*>(row + at);
+        const uint64_t lo = (uint64_t)v.y << 32 | v.x, hi = (uint64_t)v.w << 32 | v.z;
+        const int bits = (by & 3) * 16;
+        const uint64_t a = by & 4 ? hi : lo, b = by & 4 ? 0 : hi;
+        const uint64_t x = by >= 8 ? 0 : bits == 0 ? a : a >> bits | b << (64 - bits), y = by >= 8 ? 0 : b >> bits;
+        return u32x4{(uint32_t)x, (uint32_t)(x >> 32), (uint32_t)y, (uint32_t)(y >> 32)};
     }
-    const uint16_t* p = row + k;
-    if (k + 8 <= n) return *reinterpret_cast<const u32x4_half*>(p);
     uint32_t d[4] = {0, 0, 0, 0};
-    if (k < n)
 #pragma unroll
-        for (int i = 0; i < 7; ++i) {                    // (all asked for at once)
-            const uint32_t v = p[min(i, n - 1 - k)];
-            d[i >> 1] |= (k + i < n ? v : 0) << (16 * (i & 1));
-        }
+    for (int i = 0; i < 7; ++i) {
+        const uint32_t v = row[min(k + i, n - 1)];
+        d[i >> 1] |= (k + i < n ? v : 0) << (16 * (i & 1));
+    }
     return u32x4{d[0], d[1], d[2], d[3]};
 }
 
@@ -178,6 +184,7 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs g)
                     for (int q = 0; q < RR; ++q) v[j][1 + q][h] = *reinterpret_cast<const u32x4_half*>(a[q][h] + k);
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int j = 0; j < U; ++j)
                 if (s + j < s1) multiply(v[j]);
@@ -211,35 +218,60 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs g)
 // all lanes along them, so that few tokens of many adapters read each adapter
 // once and nothing else.
 // ---------------------------------------------------------------------------
+constexpr int kDotRows = 4, kDotLoads = 5;               // rows, and loads of each in flight
+constexpr int kDotStep = 512 * kDotLoads;                // values of K a wave asks for at once
+
+struct DotLoads {
+    u32x4 x[kDotLoads], a[kDotRows][kDotLoads];
+};
+
+// Rows r0 .. r0 + 3 of adapter i and token m, from value k0.
 template <bool EVEN>
-__device__ __forceinline__ f32x4 dot_rows(const LoraArgs& g, int i, int64_t m, int r0)
+__device__ __forceinline__ void dot_load(const LoraArgs& g, int i, int64_t m, int r0, int k0, DotLoads& v)
 {
-    constexpr int Q = 4, U = 5;                          // rows, and loads of each in flight
-    const int lane = threadIdx.x & 63;
     const uint16_t* x = g.x + (size_t)m * g.K;
-    const uint16_t* a[Q];
+    const uint16_t* a = g.a + (size_t)i * g.r * g.K;
 #pragma unroll
-    for (int q = 0; q < Q; ++q) a[q] = g.a + ((size_t)i * g.r + min(r0 + q, g.r - 1)) * g.K;
-    float acc[Q] = {};
-    for (int k0 = 0; k0 < g.K; k0 += 512 * U) {
-        u32x4 xv[U], av[Q][U];
+    for (int c = 0; c < kDotLoads; ++c) {
+        const int k = k0 + (c * 64 + (threadIdx.x & 63)) * 8;
+        v.x[c] = load_bf16x8<EVEN>(x, k, g.K);
 #pragma unroll
-        for (int c = 0; c < U; ++c) {
-            const int k = k0 + (c * 64 + lane) * 8;
-            xv[c] = load_bf16x8<EVEN>(x, k, g.K);
-#pragma unroll
-            for (int q = 0; q < Q; ++q) av[q][c] = load_bf16x8<EVEN>(a[q], k, g.K);
-        }
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-#pragma unroll
-            for (int c = 0; c < U; ++c) acc[q] = dot8(av[q][c], xv[c], acc[q]);
+        for (int q = 0; q < kDotRows; ++q) v.a[q][c] = load_bf16x8<EVEN>(a + (size_t)min(r0 + q, g.r - 1) * g.K, k, g.K);
     }
+    __builtin_amdgcn_sched_barrier(0);                   // (left alone, some are asked for one by one, where they are used)
+}
+
+template <bool EVEN>
+__device__ __forceinline__ void dot_add(const LoraArgs& g, int k0, DotLoads& v, float (&acc)[kDotRows])
+{
+#pragma unroll
+    for (int c = 0; c < kDotLoads; ++c)
+        if (EVEN && k0 + (c * 64 + (int)(threadIdx.x & 63)) * 8 >= g.K) v.x[c] = u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int q = 0; q < kDotRows; ++q)
+#pragma unroll
+        for (int c = 0; c < kDotLoads; ++c) acc[q] = dot8(v.a[q][c], v.x[c], acc[q]);
+}
+
+__device__ __forceinline__ f32x4 dot_sum(const LoraArgs& g, int i, const float (&acc)[kDotRows])
+{
     const float scale = g.scale != nullptr ? g.scale[i] : 1.0f;
     f32x4 u;
 #pragma unroll
-    for (int q = 0; q < Q; ++q) u[q] = wave_sum(acc[q]) * scale;
+    for (int q = 0; q < kDotRows; ++q) u[q] = wave_sum(acc[q]) * scale;
     return u;
+}
+
+template <bool EVEN>
+__device__ __forceinline__ f32x4 dot_rows(const LoraArgs& g, int i, int64_t m, int r0)
+{
+    float acc[kDotRows] = {};
+    for (int k0 = 0; k0 < g.K; k0 += kDotStep) {
+        DotLoads v;
+        dot_load<EVEN>(g, i, m, r0, k0, v);
+        dot_add<EVEN>(g, k0, v, acc);
+    }
+    return dot_sum(g, i, acc);
 }
 
 template <bool EVEN>
@@ -362,6 +394,7 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs g)
     };
     int held = slot == 0 ? __builtin_amdgcn_readlane(id, 0) : -1;
     if (held >= 0) load_b(held);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < UQ; ++i) {
         const int q = threadIdx.x + 256 * i, t = q / quads, c = q - t * quads;
@@ -385,6 +418,9 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs g)
 #pragma unroll
         for (int k = 0; k < RK; ++k) {
             if (k * 32 >= g.rp) break;                   // (ranks 65 to 96)
+            if (EVEN && 32 * k + quarter * 8 >= g.r)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) bv[j][k] = u32x4{0, 0, 0, 0};
 #pragma unroll
             for (int p = 2; p >= 0; --p) {
                 // (a token of another adapter has its own u here, and drops the result)
@@ -404,52 +440,72 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs g)
 }
 
 // ---------------------------------------------------------------------------
-// out of one token and 256 channels, a thread each: for few tokens, whose lanes
-// a tile of 16 would leave idle.  FUSED: every workgroup computes its token's u
-// itself (A comes from L2 after the first), which saves a launch.
+// out of one token and 256 channels, 64 a wave: for few tokens, whose lanes a
+// tile of 16 would leave idle.  L lanes share a row of B, 8 values each, so that
+// a wave's load is one piece of memory (a thread a row is 64 pieces: 63 tokens of
+// rank 118 and 11,708 channels 48 us); L loads give each lane one channel, number
+// (64 / L) (lane % L) + lane / L.  A row's last values are read with those before
+// them, which count once.  FUSED: every workgroup computes its token's u itself
+// (A comes from L2 after the first), which saves a launch.
 // ---------------------------------------------------------------------------
-template <bool BASE32, bool F32, bool FUSED, bool EVEN>
+template <bool BASE32, bool F32, bool FUSED, int L>
 __global__ __launch_bounds__(256) void lora_few_kernel(LoraArgs g)
 {
-    __shared__ f32x4 us[kMaxLoraRank / 4];
+    __shared__ float us[kMaxLoraRank];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t m = blockIdx.x % g.M, n = blockIdx.x / g.M * 256 + threadIdx.x;
+    const int part = lane % L, group = lane / L;
+    const int64_t m = blockIdx.x % g.M, n0 = blockIdx.x / g.M * 256 + wave * 64, n = n0 + part * (64 / L) + group;
     const int i = __builtin_amdgcn_readfirstlane(adapter_of(g, m));
     const size_t at = (size_t)m * g.N + min(n, g.N - 1);
-    float o = g.base != nullptr ? load_typed(g.base, BASE32 ? kTypeF32 : kTypeBf16, at) : 0.0f;
+    // (asked for in any case, so that it is not waited for behind a branch)
+    const void* src = g.base != nullptr ? g.base : BASE32 == F32 ? g.out : g.ids;
+    const size_t from = g.base != nullptr || BASE32 == F32 ? at : 0;
+    const uint32_t base = BASE32 ? static_cast<const uint32_t*>(src)[from] : static_cast<const uint16_t*>(src)[from];
+    float d = 0.0f;
     if (i >= 0) {
-        const uint16_t* b = g.b + ((size_t)i * g.N + min(n, g.N - 1)) * g.r;
-        u32x4 bv[4];                                     // 32 values of the row at a time, the first meanwhile
+        const int first = min(part * 8, max(g.r - 8, 0));   // the lane's ranks are first .. first + 7
+        u32x4 bv[L];
 #pragma unroll
-        for (int h = 0; h < 4; ++h) bv[h] = load_bf16x8<EVEN>(b, 8 * h, g.r);
-        if constexpr (FUSED) {
-            for (int r0 = wave * 4; r0 < g.rp; r0 += 16) {
-                f32x4 u = {0.0f, 0.0f, 0.0f, 0.0f};
-                if (r0 < g.r) u = dot_rows<true>(g, i, m, r0);   // (K is a multiple of 8)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) u[e] = r0 + e < g.r ? u[e] : 0.0f;
-                if (lane == 0) us[r0 / 4] = u;
+        for (int s = 0; s < L; ++s) {
+            const uint16_t* b = g.b + ((size_t)i * g.N + min(n0 + s * (64 / L) + group, g.N - 1)) * g.r;
+            bv[s] = L > 1 ? *reinterpret_cast<const u32x4_half*>(b + first) : load_bf16x8<false>(b, 0, g.r);
+        }
+        if constexpr (FUSED) {                           // (K is a multiple of 8)
+            auto put = [&](int r0, f32x4 u) {
+                if (lane < 4 && r0 + lane < g.r) us[r0 + lane] = lane == 0 ? u[0] : lane == 1 ? u[1] : lane == 2 ? u[2] : u[3];
+            };
+            if (g.r <= 16 && g.K <= kDotStep) {          // all at once: a loop would first wait for what is in flight
+                DotLoads v;
+                float acc[kDotRows] = {};
+                dot_load<true>(g, i, m, wave * 4, 0, v);
+                dot_add<true>(g, 0, v, acc);
+                put(wave * 4, dot_sum(g, i, acc));
+            } else {
+                for (int r0 = wave * 4; r0 < g.r; r0 += 16) put(r0, dot_rows<true>(g, i, m, r0));
             }
         } else {
-            for (int q = threadIdx.x; q < g.rp / 4; q += 256) us[q] = reinterpret_cast<const f32x4*>(g.u + m * g.rp)[q];
+            for (int q = threadIdx.x; q < g.r; q += 256) us[q] = g.u[m * g.rp + q];
         }
         __syncthreads();
-        float d = 0.0f;
-        for (int j = 0; j < g.rp; j += 32) {
-            if (j > 0)
+        float u[8];
 #pragma unroll
-                for (int h = 0; h < 4; ++h) bv[h] = load_bf16x8<EVEN>(b, j + 8 * h, g.r);
-#pragma unroll
-            for (int h = 0; h < 4; ++h)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t w = bv[h][e >> 1];
-                    d = fmaf(us[(j + 8 * h + e) >> 2][e & 3], __uint_as_float(e & 1 ? w & 0xFFFF0000u : w << 16), d);
-                }
+        for (int e = 0; e < 8; ++e) {
+            float v = us[first + e];                     // (first + 7 < 128, the array's size)
+            asm("" : "+v"(v));                           // (a load for a select alone becomes a branch)
+            u[e] = first + e >= part * 8 && first + e < g.r ? v : 0.0f;
         }
-        o += d;
+#pragma unroll
+        for (int s = 0; s < L; ++s) {
+            float v = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v = fmaf(u[e], __uint_as_float(e & 1 ? bv[s][e >> 1] & 0xFFFF0000u : bv[s][e >> 1] << 16), v);
+            v = group_sum<L>(v);
+            d = part == s ? v : d;
+        }
     }
     if (n >= g.N) return;
+    const float o = (g.base == nullptr ? 0.0f : BASE32 ? __uint_as_float(base) : bf16_bits_to_f32(base)) + d;
     if constexpr (F32) static_cast<float*>(g.out)[at] = o;
     else static_cast<uint16_t*>(g.out)[at] = (uint16_t)f32_to_bf16_bits(o);
 }
