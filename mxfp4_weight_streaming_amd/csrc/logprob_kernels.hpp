@@ -96,13 +96,23 @@ struct Logits16 {
         const uint32_t d = v[i >> 3][(i & 7) >> 1];
         return __uint_as_float(i & 1 ? d & 0xFFFF0000u : d << 16);
     }
-    __device__ __forceinline__ void set(int i, float x)
+    __device__ __forceinline__ void set(int i, float x)   // (of the logits' type)
     {
-        if constexpr (F32) v[i >> 2][i & 3] = __float_as_uint(x);
-        else if (i & 1) v[i >> 3][(i & 7) >> 1] |= __float_as_uint(x) & 0xFFFF0000u;
-        else v[i >> 3][(i & 7) >> 1] = __float_as_uint(x) >> 16;
+        const uint32_t d = v[i / kVec][F32 ? i & 3 : (i & 7) >> 1], n = __float_as_uint(x);
+        v[i / kVec][F32 ? i & 3 : (i & 7) >> 1] = F32 ? n : i & 1 ? (d & 0xFFFFu) | (n & 0xFFFF0000u) : (d & 0xFFFF0000u) | n >> 16;
     }
+    __device__ __forceinline__ void clear(int i) { set(i, -__builtin_inff()); }
 };
+
+// 16 bytes less the first `bits` (0 to 128, whole values).
+__device__ __forceinline__ u32x4 shift_down(u32x4 v, int bits)
+{
+    const uint64_t lo = (uint64_t)v.y << 32 | v.x, hi = (uint64_t)v.w << 32 | v.z;
+    const int by = bits & 63;
+    const uint64_t a = bits >= 64 ? hi : lo, b = bits >= 64 ? 0 : hi;
+    const uint64_t x = by == 0 ? a : a >> by | b << (64 - by), y = b >> by;
+    return u32x4{(uint32_t)x, (uint32_t)(x >> 32), (uint32_t)y, (uint32_t)(y >> 32)};
+}
 
 typedef uint32_t u32x4_at __attribute__((ext_vector_type(4), aligned(2)));   // at any element
 
@@ -174,15 +184,27 @@ struct LogitWalk {
                 x.v[u] = *reinterpret_cast<const u32x4_at*>(row + (size_t)(at + (u * 64 + lane) * E) * B);
             return;
         }
+        // The row's end: a vector that would pass it is the row's last one, shifted
+        // down, with -inf behind; all are asked for before one is waited for.
+        if (V >= E) {
 #pragma unroll
-        for (int u = 0; u < Logits16<F32>::kVecs; ++u) {
-            const int p = at + (u * 64 + lane) * E;
-            if (p + E <= V) {
-                x.v[u] = *reinterpret_cast<const u32x4_at*>(row + (size_t)p * B);
-            } else {
+            for (int u = 0; u < Logits16<F32>::kVecs; ++u)
+                x.v[u] = *reinterpret_cast<const u32x4_at*>(row + (size_t)min(at + (u * 64 + lane) * E, V - E) * B);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int u = 0; u < Logits16<F32>::kVecs; ++u) {
+                const int p = at + (u * 64 + lane) * E;
+                x.v[u] = shift_down(x.v[u], min(max(p - (V - E), 0), E) * 8 * B);
 #pragma unroll
                 for (int e = 0; e < E; ++e)
-                    x.set(u * E + e, p + e < V ? load_typed(row, F32 ? kTypeF32 : kTypeBf16, p + e) : -__builtin_inff());
+                    if (p + e >= V) x.clear(u * E + e);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int p = at + (i / E * 64 + lane) * E + i % E;
+                x.clear(i);
+                if (p < V) x.set(i, load_typed(row, F32 ? kTypeF32 : kTypeBf16, p));
             }
         }
     }
@@ -332,7 +354,7 @@ __device__ __forceinline__ uint32_t lane_order(float x) { return (float_order(x)
 __device__ __forceinline__ float kth_bound(uint32_t mine, const uint32_t (&all)[64], int K)
 {
     int place = 0;
-#pragma unroll 16
+#pragma unroll 32
     for (int j = 0; j < 64; ++j) place += all[j] > mine ? 1 : 0;
     const int lane = (int)__builtin_ctzll(__ballot(place == K - 1));
     const uint32_t order = (uint32_t)__builtin_amdgcn_readlane((int)mine, lane) & ~63u;
@@ -367,14 +389,6 @@ __device__ __forceinline__ void finish_row(const LogprobArgs& g, int64_t m, cons
         for (int i = 1; i < T / 64; ++i) column = fmaxf(column, lds.columns[lane + 64 * i]);
         lds.bests[lane] = lane_order(column);
     }
-    if (wave == T / kWave - 1) {                         // the sums meanwhile
-        const RowSums r = sum_of();
-        const double log_s = finish_sums(g, m, r, a);
-        if (lane == 0) {
-            lds.m = r.m;
-            lds.log_s = log_s;
-        }
-    }
     __syncthreads();
     const float bound = kth_bound(lds.bests[lane], lds.bests, K);
     if (best >= bound && best > -inf) {
@@ -387,8 +401,15 @@ __device__ __forceinline__ void finish_row(const LogprobArgs& g, int64_t m, cons
     }
     __syncthreads();
     const int n_groups = lds.n_groups;
-    if (n_groups <= kLogprobGroupList) {
-        for (int j = tid; j < n_groups * 16; j += T) {
+    if (wave == T / kWave - 1) {                         // the sums, while the other waves read the groups again
+        const RowSums r = sum_of();
+        const double log_s = finish_sums(g, m, r, a);
+        if (lane == 0) {
+            lds.m = r.m;
+            lds.log_s = log_s;
+        }
+    } else if (n_groups <= kLogprobGroupList) {
+        for (int j = tid; j < n_groups * 16; j += T - kWave) {
             const int group = lds.groups[j >> 4], in = j & 15;
             const int64_t first = (int64_t)(group / TW) * g.group_segments * (16 * TW) + (group % TW >> 6) * 1024 +
                                   logit_place<F32>(group & 63, in);
