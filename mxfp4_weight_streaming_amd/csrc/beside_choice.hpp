@@ -17,6 +17,7 @@ namespace moe {
 // which all rows' waves are resident at once, 16 a compute unit; and where rows are too few for that, they are
 // split into parts of 256 threads, joined by a second kernel.
 constexpr int kLogprobMaxParts = 64;            // one lane each where they are joined
+constexpr int kLogprobJoin = 1024;              // threads that join a row (one of 157,184, 20 alternatives: 256 11.5 us, 512 10.4, 1,024 10.1)
 constexpr int kLogprobShort = 1024;
 constexpr int64_t kLogprobWaves = 16 * kCus;
 constexpr int64_t kLogprobSplitRows = 128;      // more rows than this are not split
@@ -36,9 +37,9 @@ constexpr LogprobPlan logprob_plan(int64_t M, int V)
     // (no more waves than there are segments for)
     while (!split && p.threads < 1024 && M * p.threads / 64 * 2 <= kLogprobWaves && V > 16 * p.threads) p.threads *= 2;
     p.segments = (int)ceil_div(V, 16 * p.threads);
-    // the threads that read the groups' maxima hold 16 each: 1,024 of a row in
-    // parts, else those that wrote them
-    p.group_segments = (int)ceil_div(p.segments, split ? 64 : 16);
+    // the groups' maxima end up in registers: 64 times 256 of a row in parts, 16 a
+    // thread of one that has just been walked
+    p.group_segments = (int)ceil_div(p.segments, split ? kLogprobMaxParts : 16);
     p.groups = (int)ceil_div(p.segments, p.group_segments);
     const int64_t parts = split ? std::min<int64_t>({ceil_div(1024, M), kLogprobMaxParts, p.groups}) : 1;
     p.part_segments = (int)ceil_div(p.groups, parts) * p.group_segments;   // whole groups

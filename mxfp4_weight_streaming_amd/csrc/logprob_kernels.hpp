@@ -24,6 +24,7 @@
 #include <type_traits>
 
 #include "around_common.hpp"
+#include "beside_choice.hpp"
 
 namespace moe {
 
@@ -318,8 +319,9 @@ struct LogprobLds {
     RowSums parts[T / kWave];
     float columns[T];
     uint32_t bests[64];
+    float bound;
     int32_t groups[kLogprobGroupList];
-    uint64_t cands[kLogprobCandidates];      // order of the logit, then the index backwards
+    alignas(16) uint64_t cands[kLogprobCandidates];   // order of the logit, then the index backwards; zeros behind the last
     double log_s;
     float m;
     int32_t n_groups, n_cands;
@@ -354,19 +356,30 @@ __device__ __forceinline__ uint32_t lane_order(float x) { return (float_order(x)
 __device__ __forceinline__ float kth_bound(uint32_t mine, const uint32_t (&all)[64], int K)
 {
     int place = 0;
-#pragma unroll 32
+#pragma unroll 16
     for (int j = 0; j < 64; ++j) place += all[j] > mine ? 1 : 0;
     const int lane = (int)__builtin_ctzll(__ballot(place == K - 1));
     const uint32_t order = (uint32_t)__builtin_amdgcn_readlane((int)mine, lane) & ~63u;
     return order > 0x007FFFFFu ? order_float(order) : -__builtin_inff();   // (-inf's order; none below it is a number's)
 }
 
+// How many of the n keys are larger; the list ends in zeros up to a multiple of 16.
+__device__ __forceinline__ int key_place(const uint64_t* keys, int n, uint64_t own)
+{
+    int place = 0;
+    for (int j = 0; j < n; j += 16)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) place += keys[j + k] > own ? 1 : 0;
+    return place;
+}
+
 // A row's outputs, by a workgroup of T threads: sum_of() gives a wave the row's
 // sums (behind the first barrier), largest[] are a thread's groups' maxima,
-// group i * T + thread of those that TW threads of the walk wrote.
-template <bool F32, int T, int TW, typename SumOf>
-__device__ __forceinline__ void finish_row(const LogprobArgs& g, int64_t m, const Asked& a, const float (&largest)[16],
-                                           LogprobLds<T>& lds, SumOf sum_of)
+// number i * T + thread of those that the walk's TW threads wrote, of which there
+// are `rows` times T at most.
+template <bool F32, int T, int TW, int NG, typename SumOf>
+__device__ __forceinline__ void finish_row(const LogprobArgs& g, int64_t m, const Asked& a, const float (&largest)[NG],
+                                           int rows, LogprobLds<T>& lds, SumOf sum_of)
 {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const float inf = __builtin_inff();
@@ -377,26 +390,41 @@ __device__ __forceinline__ void finish_row(const LogprobArgs& g, int64_t m, cons
         if (wave == T / kWave - 1) finish_sums(g, m, sum_of(), a);
         return;
     }
-    float best = largest[0];
+    float best = -inf;
 #pragma unroll
-    for (int i = 1; i < 16; ++i) best = fmaxf(best, largest[i]);
+    for (int c = 0; c < NG; c += 8)
+        if (c < rows)
+#pragma unroll
+            for (int i = c; i < c + 8; ++i) best = fmaxf(best, largest[i]);
     lds.columns[tid] = best;
     if (tid == 0) lds.n_groups = lds.n_cands = 0;
+    for (int c = tid; c < kLogprobCandidates; c += T) lds.cands[c] = 0;
     __syncthreads();
-    if (wave == 0) {
+    if (wave == 0) {                                     // (one wave: they would all be at the same work, in turn)
         float column = lds.columns[lane];
 #pragma unroll
         for (int i = 1; i < T / 64; ++i) column = fmaxf(column, lds.columns[lane + 64 * i]);
-        lds.bests[lane] = lane_order(column);
+        const uint32_t order = lane_order(column);
+        lds.bests[lane] = order;
+        __builtin_amdgcn_wave_barrier();
+        const float bound = kth_bound(order, lds.bests, K);
+        if (lane == 0) lds.bound = bound > -inf ? bound : -kLargestLogit;   // (-inf itself is not available)
     }
     __syncthreads();
-    const float bound = kth_bound(lds.bests[lane], lds.bests, K);
-    if (best >= bound && best > -inf) {
+    const float bound = lds.bound;
+    if (best >= bound) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (largest[i] >= bound && largest[i] > -inf) {
-                const int at = atomicAdd(&lds.n_groups, 1);
-                if (at < kLogprobGroupList) lds.groups[at] = i * T + tid;
+        for (int c = 0; c < NG; c += 8)
+            if (c < rows) {
+                uint32_t hits = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) hits |= largest[c + i] >= bound ? 1u << i : 0u;
+                while (hits != 0) {
+                    const int i = __builtin_ctz(hits);
+                    hits &= hits - 1;
+                    const int at = atomicAdd(&lds.n_groups, 1);
+                    if (at < kLogprobGroupList) lds.groups[at] = (c + i) * T + tid;
+                }
             }
     }
     __syncthreads();
@@ -417,7 +445,7 @@ __device__ __forceinline__ void finish_row(const LogprobArgs& g, int64_t m, cons
                 const int64_t p = first + q * (16 * TW);
                 if (p >= g.V) break;
                 const float x = logit_at(row, F32, (size_t)p);
-                if (x >= bound && x > -inf) {
+                if (x >= bound) {
                     const int at = atomicAdd(&lds.n_cands, 1);
                     if (at < kLogprobCandidates) lds.cands[at] = (uint64_t)float_order(x) << 32 | (uint32_t)~p;
                 }
@@ -435,9 +463,7 @@ __device__ __forceinline__ void finish_row(const LogprobArgs& g, int64_t m, cons
     if (n_groups <= kLogprobGroupList && n_cands <= kLogprobCandidates) {
         for (int c = tid; c < n_cands; c += T) {
             const uint64_t own = lds.cands[c];
-            int at = 0;
-#pragma unroll 4
-            for (int j = 0; j < n_cands; ++j) at += lds.cands[j] > own ? 1 : 0;
+            const int at = key_place(lds.cands, n_cands, own);
             if (at < K) put(at, order_float((uint32_t)(own >> 32)), (int)~(uint32_t)own);
         }
         for (int k = n_cands + tid; k < K; k += T) put(k, -inf, -1);
@@ -517,16 +543,17 @@ __device__ __forceinline__ RowSums walk_row(const LogprobArgs& g, int64_t m, int
 
 __device__ __forceinline__ RowSums no_sums() { return RowSums{0.0, 0.0, -__builtin_inff(), 0, 0, 0}; }
 
-// The largest logits of a thread's groups.
-template <int T>
-__device__ __forceinline__ void load_maxima(const float* maxima, int n, float (&largest)[16])
+// The largest logits of n groups, i * T + thread in largest[i].
+template <int T, int NG>
+__device__ __forceinline__ void load_maxima(const float* maxima, int n, float (&largest)[NG])
 {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int at = i * T + (int)threadIdx.x;
-        const float x = maxima[min(at, n - 1)];
-        largest[i] = at < n ? x : -__builtin_inff();
-    }
+    for (int c = 0; c < NG; c += 8)
+        if (c * T < n)
+#pragma unroll
+            for (int i = c; i < c + 8; ++i) largest[i] = maxima[min(i * T + (int)threadIdx.x, n - 1)];
+#pragma unroll
+    for (int i = 0; i < NG; ++i) largest[i] = i * T + (int)threadIdx.x < n ? largest[i] : -__builtin_inff();
 }
 
 // A workgroup of T threads a row, from the logits to the outputs.
@@ -542,7 +569,7 @@ __global__ __launch_bounds__(T, 4) void logprob_rows_kernel(LogprobArgs g)
         if (lane == 0) lds.parts[threadIdx.x >> 6] = r;
         float largest[16] = {};
         if (g.topk > 0) load_maxima<T>(maxima, g.groups * T, largest);   // (a thread reads what it wrote itself)
-        finish_row<F32, T, T>(g, m, a, largest, lds,
+        finish_row<F32, T, T>(g, m, a, largest, g.groups, lds,
                               [&] { return join_sums(lane < T / kWave ? lds.parts[lane] : no_sums()); });
         __syncthreads();
     }
@@ -569,20 +596,21 @@ __global__ __launch_bounds__(256, 5) void logprob_parts_kernel(LogprobArgs g)
 // A workgroup a row (a wave, where no alternatives are asked for), from its
 // parts to the outputs.
 template <bool F32>
-__global__ __launch_bounds__(1024) void logprob_join_kernel(LogprobArgs g)
+__global__ __launch_bounds__(kLogprobJoin) void logprob_join_kernel(LogprobArgs g)
 {
-    __shared__ LogprobLds<1024> lds;
-    const int lane = threadIdx.x & 63;
+    constexpr int T = kLogprobJoin;
+    __shared__ LogprobLds<T> lds;
+    const int lane = threadIdx.x & 63, n = g.groups * 256;
     const int64_t m = blockIdx.x;
-    float largest[16] = {};
-    const Asked a = asked_of<F32>(g, m, row_of<F32>(g, m));
+    float largest[kLogprobMaxParts * 256 / T] = {};
+    if (g.topk > 0) load_maxima<T>(g.maxima + m * n, n, largest);
     const RowSums mine = lane < g.parts ? g.sums[m * g.parts + lane] : no_sums();
+    const Asked a = asked_of<F32>(g, m, row_of<F32>(g, m));
     if (g.topk == 0) {
         finish_sums(g, m, join_sums(mine), a);
         return;
     }
-    load_maxima<1024>(g.maxima + m * g.groups * 256, g.groups * 256, largest);
-    finish_row<F32, 1024, 256>(g, m, a, largest, lds, [&] { return join_sums(mine); });
+    finish_row<F32, T, 256>(g, m, a, largest, (n + T - 1) / T, lds, [&] { return join_sums(mine); });
 }
 
 // A wave a row of at most 1,024 logits: they stay in its registers, and its
@@ -591,7 +619,7 @@ template <bool F32>
 __global__ __launch_bounds__(256, 4) void logprob_short_kernel(LogprobArgs g)
 {
     __shared__ uint32_t bests[4][64];
-    __shared__ uint64_t cands[4][kLogprobShortList];
+    __shared__ alignas(16) uint64_t cands[4][kLogprobShortList];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const float inf = __builtin_inff();
     const int64_t m = (int64_t)blockIdx.x * 4 + wave;
@@ -617,6 +645,8 @@ __global__ __launch_bounds__(256, 4) void logprob_short_kernel(LogprobArgs g)
         g.topk_logprob[m * K + k] = i < 0 ? -inf : log_p(x, r.m, log_s);
     };
     bests[wave][lane] = lane_order(best);
+#pragma unroll
+    for (int c = 0; c < kLogprobShortList; c += 64) cands[wave][c + lane] = 0;
     __builtin_amdgcn_wave_barrier();
     const float bound = kth_bound(bests[wave][lane], bests[wave], K);
     int n = 0;
@@ -636,9 +666,7 @@ __global__ __launch_bounds__(256, 4) void logprob_short_kernel(LogprobArgs g)
     if (n <= kLogprobShortList) {
         for (int c = lane; c < n; c += 64) {
             const uint64_t own = cands[wave][c];
-            int at = 0;
-#pragma unroll 4
-            for (int j = 0; j < n; ++j) at += cands[wave][j] > own ? 1 : 0;
+            const int at = key_place(cands[wave], n, own);
             if (at < K) put(at, order_float((uint32_t)(own >> 32)), (int)~(uint32_t)own);
         }
         for (int k = n + lane; k < K; k += 64) put(k, -inf, -1);

@@ -61,7 +61,7 @@ hipError_t launch(LogprobArgs a, hipStream_t s)
     hipLaunchKernelGGL((logprob_parts_kernel<F32>), dim3((unsigned)(a.M * p.parts)), dim3(256), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((logprob_join_kernel<F32>), dim3((unsigned)a.M), dim3(a.topk > 0 ? 1024 : 64), 0, s, a);
+    hipLaunchKernelGGL((logprob_join_kernel<F32>), dim3((unsigned)a.M), dim3(a.topk > 0 ? kLogprobJoin : 64), 0, s, a);
     return hipGetLastError();
 }
 
