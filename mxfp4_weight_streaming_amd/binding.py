@@ -670,12 +670,15 @@ def moe_lora_workspace_bytes(lp: MoeLora, max_tokens: int) -> int:
     return _lib.moe_lora_workspace_bytes(ctypes.byref(lp), max_tokens)
 
 
-def lora_workspace(lp: MoeLora, max_tokens: int):
-    """A workspace (allocated through torch) for up to max_tokens tokens."""
+def lora_workspace(lp: MoeLora, max_tokens: int, product: bool = True):
+    """A workspace (allocated through torch) for up to max_tokens tokens; for moe_lora_add alone where product is false,
+    which takes much less."""
     import torch
     n = moe_lora_workspace_bytes(lp, max_tokens)
     if n == 0:
         raise MoeError(MOE_ERR_INVALID_ARG, "moe_lora_workspace_bytes")
+    if not product:
+        n = (max_tokens * ((lp.rank + 31) // 32) * 32 * 4 + 255) // 256 * 256
     return torch.empty(n, dtype=torch.uint8, device=lp.held[0].device)
 
 

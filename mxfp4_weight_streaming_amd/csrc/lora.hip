@@ -88,13 +88,13 @@ hipError_t add(const LoraArgs& a, hipStream_t s)
     return p.few ? few<BASE32, F32, false>(a, s) : expand<BASE32, F32>(a, p, s);
 }
 
-size_t u_bytes(int64_t M, int r) { return align256((size_t)M * lora_padded(r) * 4); }
-
 }  // namespace
 
-size_t lora_workspace(int64_t M, int64_t N, int r)
+size_t lora_add_workspace(int64_t M, int r) { return align256((size_t)M * lora_padded(r) * 4); }
+
+size_t lora_product_workspace(int64_t M, int64_t N, int r)
 {
-    return u_bytes(M, r) + (size_t)std::min<int64_t>(M, lora_product_rows(N)) * N * 4;
+    return lora_add_workspace(M, r) + (size_t)std::min<int64_t>(M, lora_product_rows(N)) * N * 4;
 }
 
 hipError_t launch_lora_add(const LoraArgs& a, hipStream_t s)
@@ -121,7 +121,7 @@ hipError_t launch_int8_linear_lora(const Int8Args& p, const LoraArgs& a, hipStre
         if (f32) {
             l.base = l.out;
         } else {
-            g.out = reinterpret_cast<uint8_t*>(a.u) + u_bytes(a.M, a.r);
+            g.out = reinterpret_cast<uint8_t*>(a.u) + lora_add_workspace(a.M, a.r);
             l.base = g.out;
             l.out = static_cast<uint16_t*>(a.out) + (size_t)m * a.N;
         }

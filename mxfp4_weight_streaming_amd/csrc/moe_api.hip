@@ -1057,7 +1057,7 @@ moe_status moe_token_logprobs(int32_t M, int32_t V, const void* logits, int32_t 
 size_t moe_lora_workspace_bytes(const moe_lora* lora, int32_t max_tokens)
 {
     if (check_lora(lora) != MOE_OK || max_tokens <= 0) return 0;
-    return moe::lora_workspace(max_tokens, lora->out_features, lora->rank);
+    return moe::lora_product_workspace(max_tokens, lora->out_features, lora->rank);
 }
 
 moe_status moe_lora_add(const moe_lora* lora, int32_t M, const uint16_t* x, const int32_t* adapter_ids,
@@ -1069,7 +1069,7 @@ moe_status moe_lora_add(const moe_lora* lora, int32_t M, const uint16_t* x, cons
     CHECK_PTR(x); CHECK_PTR(adapter_ids); CHECK_PTR(out);
     if (!type_ok(out_type)) return fail(MOE_ERR_INVALID_ARG, "out_type %d is neither bf16 (0) nor fp32 (1)", out_type);
     CHECK_ALIGN(x); CHECK_ALIGN4(adapter_ids); CHECK_ALIGN(base); CHECK_ALIGN(out);
-    const size_t need = moe::lora_workspace(M, lora->out_features, lora->rank), L = lora->num_adapters, r = lora->rank,
+    const size_t need = moe::lora_add_workspace(M, lora->rank), L = lora->num_adapters, r = lora->rank,
                  K = lora->in_features, N = lora->out_features, n = (size_t)M * N * type_bytes(out_type);
     if ((st = check_scratch(ws, ws_bytes, need, M)) != MOE_OK) return st;
     const Range in[] = {{x, (size_t)M * K * 2, "x"},
@@ -1103,7 +1103,7 @@ moe_status moe_int8_linear_lora(const int8_t* a, const float* a_scale, const int
                     moe::kMaxInt8Depth);
     CHECK_ALIGN(a); CHECK_ALIGN(w); CHECK_ALIGN(x); CHECK_ALIGN(out);
     CHECK_ALIGN4(a_scale); CHECK_ALIGN4(w_scale); CHECK_ALIGN4(adapter_ids);
-    const size_t need = moe::lora_workspace(M, lora->out_features, lora->rank), L = lora->num_adapters, r = lora->rank,
+    const size_t need = moe::lora_product_workspace(M, lora->out_features, lora->rank), L = lora->num_adapters, r = lora->rank,
                  K = lora->in_features, N = lora->out_features;
     if ((st = check_scratch(ws, ws_bytes, need, M)) != MOE_OK) return st;
     const Range in[] = {{a, (size_t)M * K, "a"},

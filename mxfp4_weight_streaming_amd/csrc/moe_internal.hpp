@@ -133,7 +133,8 @@ hipError_t launch_int8_linear(const Int8Args& a, hipStream_t s);
 // a workspace of so many bytes.
 size_t logprob_workspace(int64_t M, int V, int topk);
 hipError_t launch_logprobs(const LogprobArgs& a, hipStream_t s);
-size_t lora_workspace(int64_t M, int64_t N, int r);
+size_t lora_add_workspace(int64_t M, int r);
+size_t lora_product_workspace(int64_t M, int64_t N, int r);
 hipError_t launch_lora_add(const LoraArgs& a, hipStream_t s);
 hipError_t launch_int8_linear_lora(const Int8Args& p, const LoraArgs& a, hipStream_t s);
 

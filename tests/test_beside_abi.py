@@ -61,6 +61,18 @@ def test_workspace_sizes(moe):
     assert sizes == sorted(sizes) and sizes[0] > 0
 
 
+@pytest.mark.parametrize("M,r", [(1, 1), (2, 16), (3, 33), (64, 128), (1000, 40)])
+def test_adding_adapters_needs_their_u_alone(moe, M, r):
+    lp = moe.MoeLora(4, r, 64, 96, A, B, None)
+    need = M * ((r + 31) // 32 * 32) * 4
+    need = (need + 255) // 256 * 256
+    assert need < moe.raw().moe_lora_workspace_bytes(ctypes.byref(lp), M)
+    # (one byte less is refused; as much is enough, so that the overlap of the workspace's first byte is what is)
+    call = lambda ws, n: moe.raw().moe_lora_add(ctypes.byref(lp), M, D, E, None, G, 0, ws, n, None)  # noqa: E731
+    assert call(H, need - 1) == -4 and "workspace" in moe.moe_last_error()
+    assert call(D, need) == -1 and "overlap" in moe.moe_last_error()
+
+
 LORA = dict(L=4, r=16, K=64, N=96, a=A, b=B, s=C)
 
 

@@ -63,6 +63,15 @@ def test_shapes(moe, M, V, k, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,V,k", [(130, 262144, 32), (130, 300007, 2), (300, 30011, 9), (600, 20011, 4), (128, 16400, 3),
+                                   (129, 16400, 3)])
+def test_shapes_of_many_rows(moe, M, V, k, dtype):
+    """Rows by 1,024, 512 and 256 threads, and on either side of where they are split."""
+    print(f"M={M} V={V} k={k}", flush=True)
+    _check(moe, *_logits(M + V + k, M, V, dtype), k)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("V,pad", [(1000, 1), (1000, 24), (1001, 2), (5003, 61), (40000, 7), (63, 1)])
 def test_rows_apart(moe, V, pad, dtype):
     """Rows at any address; what lies between them is not read: it is NaN and +inf."""
