@@ -518,7 +518,8 @@ size_t moe_lora_workspace_bytes(const moe_lora* lora, int32_t max_tokens);
  *   u = scale[i] * (A[i] x[m])      products of bf16 values summed in fp32
  *   out[m] = base[m] + B[i] u       u and the sums fp32, rounded once to out_type
  * A token whose id is outside [0, num_adapters) has no adapter: out[m] = base[m].
- * What a row becomes depends on its own token and adapter alone.
+ * What a row becomes depends on its own token and adapter alone.  A weight that
+ * is infinite may give NaN where the formula gives an infinity.
  * x [M,K] bf16 (the projection's input), adapter_ids [M] int32 in any order,
  * base [M,N] of out_type, or NULL (0); out [M,N], may be base itself.  x, base
  * and out are 16-byte aligned. */

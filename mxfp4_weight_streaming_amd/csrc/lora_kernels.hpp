@@ -94,7 +94,9 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c)
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// Two fp32 values as three pairs of bf16 that add up to them.
+// Two fp32 values as three pairs of bf16 that add up to them: each takes the 8
+// leading bits of what is left (cut off, as rounding could pass the largest
+// number).  An infinity or a NaN is the first alone.
 struct Split3 {
     uint32_t v[3];
 };
@@ -104,10 +106,12 @@ __device__ __forceinline__ Split3 split_pair(float a, float b)
     Split3 s;
 #pragma unroll
     for (int p = 0; p < 3; ++p) {
-        const uint32_t lo = f32_to_bf16_bits(a), hi = f32_to_bf16_bits(b);
-        s.v[p] = lo | hi << 16;
-        a -= bf16_bits_to_f32(lo);
-        b -= bf16_bits_to_f32(hi);
+        const uint32_t lo = __float_as_uint(a) & 0xFFFF0000u, hi = __float_as_uint(b) & 0xFFFF0000u;
+        s.v[p] = lo >> 16 | hi;
+        a -= __uint_as_float(lo);
+        b -= __uint_as_float(hi);
+        a = a == a ? a : 0.0f;
+        b = b == b ? b : 0.0f;
     }
     return s;
 }

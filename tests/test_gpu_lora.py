@@ -237,3 +237,32 @@ def test_int8_rows_keep_to_their_adapter(moe):
         same[1] = False
         assert torch.equal(outs[0][same.cuda()], outs[1][same.cuda()])
         assert not bool(torch.isfinite(outs[1][0]).any())
+
+
+@pytest.mark.parametrize("M", [1, 5, 16, 70, 600])
+@pytest.mark.parametrize("r", [1, 32, 64])
+def test_infinite_and_largest_values(moe, M, r):
+    """An activation that is infinite, and a u near fp32's largest number, give what the formula gives: all of an adapter's
+    values have one sign here, so no infinity meets its opposite."""
+    g = torch.Generator().manual_seed(M + r)
+    L, K, N = 2, 72, 130
+    pos = lambda *s: (0.5 + torch.rand(*s, generator=g)).to(torch.bfloat16)  # noqa: E731
+    a, b = pos(L, r, K), pos(L, N, r) * 2.0 ** -20
+    x = pos(M, K)
+    ids = torch.randint(0, L, (M,), generator=g).to(torch.int32)
+    x[0, 3] = torch.inf
+    x[M - 1, K - 1] = torch.inf
+    if M > 4:
+        a[0, :, 8:] = 0.0
+        a[0, :, :8] = 1.0
+        x[2] = 0.0
+        x[2, 0] = torch.finfo(torch.bfloat16).max
+        x[2, 1] = 2.0 ** 119                             # fp32's largest but for its last bits: bf16 would round it up
+        ids[2] = 0
+        ids[0] = ids[M - 1] = 1                          # (0 times infinity is NaN)
+    out = _add(moe, a, b, None, x, ids, None, torch.float32)
+    ref, err = lora_delta(x, a, b, None, ids)
+    inf = torch.isinf(ref)
+    got = out.cpu().double()
+    assert bool(inf[0].all()) and bool((got[inf] == torch.inf).all())
+    check_rows(torch.where(inf, 0.0, got), torch.where(inf, 0.0, ref), torch.where(inf, 0.0, err), torch.float32)
