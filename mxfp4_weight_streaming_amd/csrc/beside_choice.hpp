@@ -76,7 +76,7 @@ constexpr LoraPlan lora_plan(int64_t M, int64_t N, int64_t K, int r)
     LoraPlan p{};
     const int64_t tn = ceil_div(N, 256), tm = ceil_div(M, 16);
     p.few = M * lora_padded(r) <= kLoraFewValues;
-    p.fused = p.few && K % 8 == 0 && r * K <= kLoraFusedWork && M * tn <= kCus;
+    p.fused = p.few && K >= 8 && r * K <= kLoraFusedWork && M * tn <= kCus;
     p.shrink_slots = lora_slots(tm * ceil_div(r, r > 16 ? 32 : 16), kCus);
     p.expand_slots = lora_slots(tm * tn, 4 * kCus);
     return p;

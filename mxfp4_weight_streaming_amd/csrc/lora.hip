@@ -34,12 +34,12 @@ bool fits(const LoraArgs& a)
     return shrink_grid(a, p) * 512 <= kMaxThreads && expand_grid(a, p) * 256 <= kMaxThreads;
 }
 
-template <bool BASE32, bool F32, int RK, bool EVEN>
+template <bool BASE32, bool F32, int RK, bool SHORT = false>
 hipError_t expand_tiles(LoraArgs a, const LoraPlan& p, hipStream_t s)
 {
     a.slots = p.expand_slots;
     const int64_t grid = expand_grid(a, p);
-    const auto kernel = lora_expand_kernel<BASE32, F32, RK, EVEN>;
+    const auto kernel = lora_expand_kernel<BASE32, F32, RK, SHORT>;
     const uint32_t lds = 3 * 16 * (a.rp / 2 + 4) * 4;
     hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(256), lds, s, a);
     return hipGetLastError();
@@ -48,9 +48,9 @@ hipError_t expand_tiles(LoraArgs a, const LoraPlan& p, hipStream_t s)
 template <bool BASE32, bool F32>
 hipError_t expand(const LoraArgs& a, const LoraPlan& p, hipStream_t s)
 {
-    if (a.r % 8 != 0) return expand_tiles<BASE32, F32, 4, false>(a, p, s);
-    if (a.r <= 32) return expand_tiles<BASE32, F32, 1, true>(a, p, s);
-    return a.r <= 64 ? expand_tiles<BASE32, F32, 2, true>(a, p, s) : expand_tiles<BASE32, F32, 4, true>(a, p, s);
+    if (a.r < 8) return expand_tiles<BASE32, F32, 1, true>(a, p, s);
+    if (a.r <= 32) return expand_tiles<BASE32, F32, 1>(a, p, s);
+    return a.r <= 64 ? expand_tiles<BASE32, F32, 2>(a, p, s) : expand_tiles<BASE32, F32, 4>(a, p, s);
 }
 
 template <bool BASE32, bool F32, bool FUSED>
@@ -68,7 +68,7 @@ hipError_t few(const LoraArgs& a, hipStream_t s)
 hipError_t shrink(LoraArgs a, const LoraPlan& p, hipStream_t s)
 {
     if (p.few) {
-        const auto kernel = a.K % 8 == 0 ? lora_shrink_few_kernel<true> : lora_shrink_few_kernel<false>;
+        const auto kernel = a.K < 8 ? lora_shrink_few_kernel<true> : lora_shrink_few_kernel<false>;
         hipLaunchKernelGGL(kernel, dim3((unsigned)(a.M * ceil_div(a.r, 16))), dim3(256), 0, s, a);
         return hipGetLastError();
     }

@@ -40,26 +40,30 @@ __device__ __forceinline__ int adapter_of(const LoraArgs& g, int64_t m)
 // wave's 16 tokens (-1, none, too) that falls to `slot` of `slots` (a power of
 // two).
 template <typename F>
-__device__ __forceinline__ void each_adapter(int id, int slot, int slots, F f)
+__device__ __forceinline__ void each_adapter(int id, uint32_t slot, int slots, F f)
 {
     uint32_t todo = (uint32_t)__ballot(id >= -1) & 0xFFFFu;
-    for (int d = 0; todo != 0; ++d) {
+    for (uint32_t d = 0; todo != 0; ++d) {
         const int i = __builtin_amdgcn_readlane(id, (int)__builtin_ctz(todo));
         const uint32_t mask = (uint32_t)__ballot(id == i) & 0xFFFFu;
         todo &= ~mask;
-        if ((d & (slots - 1)) == slot) f(i, mask);
+        if ((d & (uint32_t)(slots - 1)) == slot) f(i, mask);
     }
 }
 
-// Values k .. k + 7 of a row of n.  EVEN: n is a multiple of 8, so they are all
-// there or none is, and what is read where none is (the row's first) is put to 0
-// by the caller, after it has asked for everything (a zero put in here would be
-// waited for at once).  Else zeros stand behind the row; a part of it comes from
-// its last 8, shifted down, and only rows shorter than 8 are read value by value.
-template <bool EVEN>
+// Workgroups are dealt to the 8 XCDs in turn, each with a cache of its own: the
+// tile of workgroup b of n, so that an XCD has consecutive tiles, which share
+// tokens and their adapter's rows.
+__device__ __forceinline__ uint32_t tile_of(uint32_t b, uint32_t n)
+{
+    const uint32_t xcd = b & 7;
+    return n / 8 * xcd + min(xcd, n & 7) + (b >> 3);
+}
+
+// Values k .. k + 7 of a row of n, and zeros behind it: a part of them comes from
+// the row's last 8, shifted down; rows shorter than 8 are read value by value.
 __device__ __forceinline__ u32x4 load_bf16x8(const uint16_t* row, int k, int n)
 {
-    if constexpr (EVEN) return *reinterpret_cast<const u32x4_half*>(row + (k < n ? k : 0));
     if (n >= 8) {
         const int at = min(k, n - 8), by = k - at;       // values to drop
         const u32x4 v = *reinterpret_cast<const u32x4_half*>(row + at);
@@ -77,6 +81,28 @@ __device__ __forceinline__ u32x4 load_bf16x8(const uint16_t* row, int k, int n)
     }
     return u32x4{d[0], d[1], d[2], d[3]};
 }
+
+// The same in the form that costs nothing before the values are there: where 8
+// would pass the row's end they are its last 8, of which the other factor counts
+// each once (drop_first, place_of).  SHORT: a row of less than 8.
+template <bool SHORT>
+__device__ __forceinline__ u32x4 load_last8(const uint16_t* row, int k, int n)
+{
+    if constexpr (SHORT) return load_bf16x8(row, k, n);
+    return *reinterpret_cast<const u32x4_half*>(row + min(k, n - 8));
+}
+
+// 0 for the first n values (any n of 8 or more: all).
+__device__ __forceinline__ u32x4 drop_first(u32x4 v, int n)
+{
+    const uint64_t lo = n >= 4 ? 0 : ~0ull << (16 * n), hi = n >= 8 ? 0 : n > 4 ? ~0ull << (16 * (n & 3)) : ~0ull;
+    return u32x4{v.x & (uint32_t)lo, v.y & (uint32_t)(lo >> 32), v.z & (uint32_t)hi, v.w & (uint32_t)(hi >> 32)};
+}
+
+// Where rank k stands in a row of u: r = 8 c + d ranks have the last d at the end
+// of their 8, behind zeros, as B's last 8 are read.
+__device__ __forceinline__ int u_gap(int r) { return r > 8 && (r & 7) != 0 ? 8 - (r & 7) : 0; }
+__device__ __forceinline__ int place_of(int k, int r) { return k + (k >= (r & ~7) ? u_gap(r) : 0); }
 
 // acc + the sum of 8 products, one after another in fp32.
 __device__ __forceinline__ float dot8(u32x4 a, u32x4 b, float acc)
@@ -116,16 +142,25 @@ __device__ __forceinline__ Split3 split_pair(float a, float b)
     return s;
 }
 
-// u of ranks k .. k + 3 of a token, zeros behind r; the 16 behind a last tile
-// that ends in the middle of 32 are cleared with it.
+// u of ranks k .. k + 3 of a token to their places, zeros where there is none; the
+// 16 behind a last tile that ends in the middle of 32 are cleared with it.
 __device__ __forceinline__ void store_u(const LoraArgs& g, int64_t m, int k, f32x4 u)
 {
     if (k >= g.rp) return;
+    float* row = g.u + (size_t)m * g.rp;
+    const int last = g.r & ~7, gap = u_gap(g.r);
+    if (gap != 0 && k >= last && k < last + 8) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) u[e] = k + e < g.r ? u[e] : 0.0f;
-    f32x4* p = reinterpret_cast<f32x4*>(g.u + (size_t)m * g.rp + k);
-    p[0] = u;
-    if (k / 16 * 16 + 16 >= g.r && k + 16 < g.rp) p[4] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int e = 0; e < 4; ++e)
+            if (k + e < g.r) row[k + e + gap] = u[e];
+        if (k == last)
+            for (int e = 0; e < gap; ++e) row[last + e] = 0.0f;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[e] = k + e < g.r ? u[e] : 0.0f;
+        *reinterpret_cast<f32x4*>(row + k) = u;
+    }
+    if (k / 16 * 16 + 16 >= g.r && k + 16 < g.rp) *reinterpret_cast<f32x4*>(row + k + 16) = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 }
 
 // ---------------------------------------------------------------------------
@@ -144,10 +179,10 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs g)
     __shared__ f32x4 part[W][RR][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = lane & 15, quarter = lane >> 4, load_row = lane >> 3, chunk = lane & 7;
-    const int ranks = (g.r + 16 * RR - 1) / (16 * RR);
-    // (workgroups go to the 8 XCDs in turn: slots, most of them idle, come last)
-    const int64_t tiles = (g.M + 15) / 16 * ranks, tile = blockIdx.x % tiles, m0 = tile / ranks * 16;
-    const int slot = (int)(blockIdx.x / tiles), r0 = (int)(tile % ranks) * 16 * RR;
+    const uint32_t ranks = (g.r + 16 * RR - 1) / (16 * RR), tiles = (uint32_t)((g.M + 15) / 16) * ranks;
+    const uint32_t slot = blockIdx.x / tiles, tile = tile_of(blockIdx.x - slot * tiles, tiles);   // (most slots are idle, and come last)
+    const int64_t m0 = (int64_t)(tile / ranks) * 16;
+    const int r0 = (int)(tile % ranks) * 16 * RR;
     const int id = adapter_of(g, m0 + row);
     const uint16_t* x[2];
 #pragma unroll
@@ -197,9 +232,9 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs g)
             u32x4 v[1 + RR][2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                v[0][h] = load_bf16x8<false>(x[h], chunks * 64 + chunk * 8, g.K);
+                v[0][h] = load_bf16x8(x[h], chunks * 64 + chunk * 8, g.K);
 #pragma unroll
-                for (int q = 0; q < RR; ++q) v[1 + q][h] = load_bf16x8<false>(a[q][h], chunks * 64 + chunk * 8, g.K);
+                for (int q = 0; q < RR; ++q) v[1 + q][h] = load_bf16x8(a[q][h], chunks * 64 + chunk * 8, g.K);
             }
             multiply(v);
         }
@@ -230,7 +265,7 @@ struct DotLoads {
 };
 
 // Rows r0 .. r0 + 3 of adapter i and token m, from value k0.
-template <bool EVEN>
+template <bool SHORT>
 __device__ __forceinline__ void dot_load(const LoraArgs& g, int i, int64_t m, int r0, int k0, DotLoads& v)
 {
     const uint16_t* x = g.x + (size_t)m * g.K;
@@ -238,19 +273,20 @@ __device__ __forceinline__ void dot_load(const LoraArgs& g, int i, int64_t m, in
 #pragma unroll
     for (int c = 0; c < kDotLoads; ++c) {
         const int k = k0 + (c * 64 + (threadIdx.x & 63)) * 8;
-        v.x[c] = load_bf16x8<EVEN>(x, k, g.K);
+        v.x[c] = load_last8<SHORT>(x, k, g.K);
 #pragma unroll
-        for (int q = 0; q < kDotRows; ++q) v.a[q][c] = load_bf16x8<EVEN>(a + (size_t)min(r0 + q, g.r - 1) * g.K, k, g.K);
+        for (int q = 0; q < kDotRows; ++q) v.a[q][c] = load_last8<SHORT>(a + (size_t)min(r0 + q, g.r - 1) * g.K, k, g.K);
     }
     __builtin_amdgcn_sched_barrier(0);                   // (left alone, some are asked for one by one, where they are used)
 }
 
-template <bool EVEN>
+template <bool SHORT>
 __device__ __forceinline__ void dot_add(const LoraArgs& g, int k0, DotLoads& v, float (&acc)[kDotRows])
 {
+    if (!SHORT && k0 + kDotStep > g.K)
 #pragma unroll
-    for (int c = 0; c < kDotLoads; ++c)
-        if (EVEN && k0 + (c * 64 + (int)(threadIdx.x & 63)) * 8 >= g.K) v.x[c] = u32x4{0, 0, 0, 0};
+        for (int c = 0; c < kDotLoads; ++c)
+            v.x[c] = drop_first(v.x[c], max(k0 + (c * 64 + (int)(threadIdx.x & 63)) * 8 - (g.K - 8), 0));
 #pragma unroll
     for (int q = 0; q < kDotRows; ++q)
 #pragma unroll
@@ -266,19 +302,19 @@ __device__ __forceinline__ f32x4 dot_sum(const LoraArgs& g, int i, const float (
     return u;
 }
 
-template <bool EVEN>
+template <bool SHORT>
 __device__ __forceinline__ f32x4 dot_rows(const LoraArgs& g, int i, int64_t m, int r0)
 {
     float acc[kDotRows] = {};
     for (int k0 = 0; k0 < g.K; k0 += kDotStep) {
         DotLoads v;
-        dot_load<EVEN>(g, i, m, r0, k0, v);
-        dot_add<EVEN>(g, k0, v, acc);
+        dot_load<SHORT>(g, i, m, r0, k0, v);
+        dot_add<SHORT>(g, k0, v, acc);
     }
     return dot_sum(g, i, acc);
 }
 
-template <bool EVEN>
+template <bool SHORT>
 __global__ __launch_bounds__(256) void lora_shrink_few_kernel(LoraArgs g)
 {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), ranks = (g.r + 15) / 16;
@@ -286,7 +322,7 @@ __global__ __launch_bounds__(256) void lora_shrink_few_kernel(LoraArgs g)
     const int i = adapter_of(g, m), r0 = (int)(blockIdx.x % ranks) * 16 + wave * 4;
     if (i < 0) return;
     f32x4 u = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (r0 < g.r) u = dot_rows<EVEN>(g, i, m, r0);
+    if (r0 < g.r) u = dot_rows<SHORT>(g, i, m, r0);
     if ((threadIdx.x & 63) == 0) store_u(g, m, r0, u);
 }
 
@@ -355,16 +391,16 @@ __device__ __forceinline__ void store_row4(void* p, size_t at, int n, const floa
     }
 }
 
-template <bool BASE32, bool F32, int RK, bool EVEN>
+template <bool BASE32, bool F32, int RK, bool SHORT>
 __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs g)
 {
     extern __shared__ uint32_t us[];                     // [3][16][rp / 2 + 4]
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = lane & 15, quarter = lane >> 4, stride = g.rp / 2 + 4;
-    const int64_t tn = (g.N + 255) / 256, tm = (g.M + 15) / 16;
-    const int64_t tile = blockIdx.x % (tm * tn), m0 = tile / tn * 16;
-    const int64_t n0 = tile % tn * 256 + wave * 64, n = n0 + row * 4;
-    const int slot = (int)(blockIdx.x / (tm * tn)), left = (int)max((int64_t)0, min((int64_t)4, g.N - n));
+    const uint32_t tn = (uint32_t)((g.N + 255) / 256), tiles = (uint32_t)((g.M + 15) / 16) * tn;
+    const uint32_t slot = blockIdx.x / tiles, tile = tile_of(blockIdx.x - slot * tiles, tiles);
+    const int64_t m0 = (int64_t)(tile / tn) * 16, n0 = (int64_t)(tile % tn) * 256 + wave * 64, n = n0 + row * 4;
+    const int left = (int)max((int64_t)0, min((int64_t)4, g.N - n));
     const int id = adapter_of(g, m0 + row);
     if (slot > 0) {
         bool any = false;
@@ -393,7 +429,7 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs g)
         for (int j = 0; j < 4; ++j) {
             const uint16_t* b = g.b + ((size_t)i * g.N + min(n + j, g.N - 1)) * g.r;
 #pragma unroll
-            for (int k = 0; k < RK; ++k) bv[j][k] = load_bf16x8<EVEN>(b, 32 * k + quarter * 8, g.r);
+            for (int k = 0; k < RK; ++k) bv[j][k] = load_last8<SHORT>(b, 32 * k + quarter * 8, g.r);
         }
     };
     int held = slot == 0 ? __builtin_amdgcn_readlane(id, 0) : -1;
@@ -422,9 +458,6 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs g)
 #pragma unroll
         for (int k = 0; k < RK; ++k) {
             if (k * 32 >= g.rp) break;                   // (ranks 65 to 96)
-            if (EVEN && 32 * k + quarter * 8 >= g.r)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) bv[j][k] = u32x4{0, 0, 0, 0};
 #pragma unroll
             for (int p = 2; p >= 0; --p) {
                 // (a token of another adapter has its own u here, and drops the result)
@@ -472,23 +505,23 @@ __global__ __launch_bounds__(256) void lora_few_kernel(LoraArgs g)
 #pragma unroll
         for (int s = 0; s < L; ++s) {
             const uint16_t* b = g.b + ((size_t)i * g.N + min(n0 + s * (64 / L) + group, g.N - 1)) * g.r;
-            bv[s] = L > 1 ? *reinterpret_cast<const u32x4_half*>(b + first) : load_bf16x8<false>(b, 0, g.r);
+            bv[s] = L > 1 ? *reinterpret_cast<const u32x4_half*>(b + first) : load_bf16x8(b, 0, g.r);
         }
-        if constexpr (FUSED) {                           // (K is a multiple of 8)
+        if constexpr (FUSED) {                           // (K is 8 or more)
             auto put = [&](int r0, f32x4 u) {
                 if (lane < 4 && r0 + lane < g.r) us[r0 + lane] = lane == 0 ? u[0] : lane == 1 ? u[1] : lane == 2 ? u[2] : u[3];
             };
             if (g.r <= 16 && g.K <= kDotStep) {          // all at once: a loop would first wait for what is in flight
                 DotLoads v;
                 float acc[kDotRows] = {};
-                dot_load<true>(g, i, m, wave * 4, 0, v);
-                dot_add<true>(g, 0, v, acc);
+                dot_load<false>(g, i, m, wave * 4, 0, v);
+                dot_add<false>(g, 0, v, acc);
                 put(wave * 4, dot_sum(g, i, acc));
             } else {
-                for (int r0 = wave * 4; r0 < g.r; r0 += 16) put(r0, dot_rows<true>(g, i, m, r0));
+                for (int r0 = wave * 4; r0 < g.r; r0 += 16) put(r0, dot_rows<false>(g, i, m, r0));
             }
         } else {
-            for (int q = threadIdx.x; q < g.r; q += 256) us[q] = g.u[m * g.rp + q];
+            for (int q = threadIdx.x; q < g.r; q += 256) us[q] = g.u[m * g.rp + place_of(q, g.r)];
         }
         __syncthreads();
         float u[8];
