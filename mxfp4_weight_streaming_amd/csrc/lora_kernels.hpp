@@ -394,6 +394,7 @@ __device__ __forceinline__ void store_row4(void* p, size_t at, int n, const floa
 template <bool BASE32, bool F32, int RK, bool SHORT>
 __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs g)
 {
+    __shared__ u32x4 stage[4][4 * RK][64];
     extern __shared__ uint32_t us[];                     // [3][16][rp / 2 + 4]
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = lane & 15, quarter = lane >> 4, stride = g.rp / 2 + 4;
@@ -427,9 +428,9 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs g)
     auto load_b = [&](int i) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint16_t* b = g.b + ((size_t)i * g.N + min(n + j, g.N - 1)) * g.r;
+            const uint16_t* b = g.b + ((size_t)i * g.N + min(n0 + (lane >> 2) * 4 + j, g.N - 1)) * g.r;
 #pragma unroll
-            for (int k = 0; k < RK; ++k) bv[j][k] = load_last8<SHORT>(b, 32 * k + quarter * 8, g.r);
+            for (int k = 0; k < RK; ++k) bv[j][k] = load_last8<SHORT>(b, 32 * k + (lane & 3) * 8, g.r);
         }
     };
     int held = slot == 0 ? __builtin_amdgcn_readlane(id, 0) : -1;
@@ -456,14 +457,21 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs g)
         if (i != held) load_b(held = i);
         f32x4 acc[4] = {};
 #pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int k = 0; k < RK; ++k) stage[wave][j * RK + k][lane ^ ((lane >> 3) & 3)] = bv[j][k];
+#pragma unroll
         for (int k = 0; k < RK; ++k) {
             if (k * 32 >= g.rp) break;                   // (ranks 65 to 96)
+            u32x4 bw[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) bw[j] = stage[wave][j * RK + k][row * 4 + (quarter ^ ((row >> 1) & 3))];
 #pragma unroll
             for (int p = 2; p >= 0; --p) {
                 // (a token of another adapter has its own u here, and drops the result)
                 const u32x4 uv = *reinterpret_cast<const u32x4*>(us + (p * 16 + row) * stride + 16 * k + quarter * 4);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[j] = mfma(uv, bv[j][k], acc[j]);
+                for (int j = 0; j < 4; ++j) acc[j] = mfma(uv, bw[j], acc[j]);
             }
         }
 #pragma unroll
