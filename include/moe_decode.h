@@ -495,7 +495,8 @@ moe_status moe_token_logprobs(int32_t M, int32_t V, const void* logits, int32_t 
 
 /* Low-rank adapters of one projection, K = in_features to N = out_features, all
  * of one rank r (pad smaller ones with zeros): num_adapters 1..65535, rank
- * 1..128.  Device memory owned by the caller; a and b are 16-byte aligned. */
+ * 1..128, K up to 2^24.  Device memory owned by the caller; a and b are 16-byte
+ * aligned. */
 typedef struct {
     int32_t num_adapters;
     int32_t rank;

@@ -16,6 +16,7 @@ constexpr int kMaxGroups = 64;          // one lane a group
 constexpr int kMaxAlternatives = 32;    // top alternatives of a row of logits
 constexpr int64_t kMaxRowStride = 1ll << 30;   // elements between rows of logits
 constexpr int kMaxLoraRank = 128;
+constexpr int kMaxLoraDepth = 1 << 24;   // (32 rows are addressed with 32 bits)
 constexpr int kMaxAdapters = 65535;
 constexpr int kMaxInt8Depth = 131071;   // 131071 * 128 * 128 < 2^31
 

@@ -184,59 +184,75 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs g)
     const int64_t m0 = (int64_t)(tile / ranks) * 16;
     const int r0 = (int)(tile % ranks) * 16 * RR;
     const int id = adapter_of(g, m0 + row);
-    const uint16_t* x[2];
+    // (addresses as a uniform part and 32 bits of a lane's own: 64 bits each would
+    // take the registers that the loads in flight need)
+    const uint16_t* x = g.x + (size_t)m0 * g.K;
+    uint32_t xo[2], ao[RR][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) x[h] = g.x + (size_t)min(m0 + h * 8 + load_row, g.M - 1) * g.K;
+    for (int h = 0; h < 2; ++h) {
+        xo[h] = (uint32_t)min((int64_t)(h * 8 + load_row), g.M - 1 - m0) * (uint32_t)g.K;
+#pragma unroll
+        for (int q = 0; q < RR; ++q) ao[q][h] = (uint32_t)min(q * 16 + h * 8 + load_row, g.r - 1 - r0) * (uint32_t)g.K;
+    }
     const int chunks = g.K / 64, s0 = chunks * wave / W, s1 = chunks * (wave + 1) / W;
-    each_adapter(id, slot, g.slots, [&](int i, uint32_t mask) {
-        if (i < 0) return;
-        const uint16_t* a[RR][2];
+    // x's values are asked for before the adapter is known, and where they are
+    // all a wave needs they serve every adapter of the tile.
+    u32x4 xv[U][2];
+    int held = s0;
+    auto load_x = [&](int s) {
 #pragma unroll
-        for (int q = 0; q < RR; ++q)
+        for (int j = 0; j < U; ++j)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                a[q][h] = g.a + ((size_t)i * g.r + min(r0 + q * 16 + h * 8 + load_row, g.r - 1)) * g.K;
+                xv[j][h] = *reinterpret_cast<const u32x4_half*>(x + min(s + j, s1 - 1) * 64 + (xo[h] + chunk * 8));
+        held = s;
+    };
+    if (s0 < s1) load_x(s0);
+    __builtin_amdgcn_sched_barrier(0);
+    each_adapter(id, slot, g.slots, [&](int i, uint32_t mask) {
+        if (i < 0) return;
+        const uint16_t* a = g.a + ((size_t)i * g.r + r0) * g.K;
         f32x4 acc[RR] = {};
-        auto multiply = [&](const u32x4 (&v)[1 + RR][2]) {
+        auto multiply = [&](const u32x4 (&xj)[2], const u32x4 (&aj)[RR][2]) {
 #pragma unroll
-            for (int q = 0; q < 1 + RR; ++q)
+            for (int h = 0; h < 2; ++h) {
+                const int at = (h * 8 + load_row) * 8 + (chunk ^ (load_row & 7));
+                stage[wave][0][at] = xj[h];
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    stage[wave][q][(h * 8 + load_row) * 8 + (chunk ^ (load_row & 7))] = v[q][h];
+                for (int q = 0; q < RR; ++q) stage[wave][1 + q][at] = aj[q][h];
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int at = row * 8 + ((h * 4 + quarter) ^ (row & 7));
-                const u32x4 xv = stage[wave][0][at];
+                const u32x4 b = stage[wave][0][at];
 #pragma unroll
-                for (int q = 0; q < RR; ++q) acc[q] = mfma(stage[wave][1 + q][at], xv, acc[q]);
+                for (int q = 0; q < RR; ++q) acc[q] = mfma(stage[wave][1 + q][at], b, acc[q]);
             }
         };
         for (int s = s0; s < s1; s += U) {
-            u32x4 v[U][1 + RR][2];
+            if (s != held) load_x(s);
+            u32x4 av[U][RR][2];
 #pragma unroll
-            for (int j = 0; j < U; ++j) {
-                const int k = min(s + j, s1 - 1) * 64 + chunk * 8;
+            for (int j = 0; j < U; ++j)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    v[j][0][h] = *reinterpret_cast<const u32x4_half*>(x[h] + k);
+                for (int q = 0; q < RR; ++q)
 #pragma unroll
-                    for (int q = 0; q < RR; ++q) v[j][1 + q][h] = *reinterpret_cast<const u32x4_half*>(a[q][h] + k);
-                }
-            }
+                    for (int h = 0; h < 2; ++h)
+                        av[j][q][h] = *reinterpret_cast<const u32x4_half*>(a + min(s + j, s1 - 1) * 64 + (ao[q][h] + chunk * 8));
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int j = 0; j < U; ++j)
-                if (s + j < s1) multiply(v[j]);
+                if (s + j < s1) multiply(xv[j], av[j]);
         }
         if (wave == W - 1 && chunks * 64 < g.K) {
-            u32x4 v[1 + RR][2];
+            u32x4 xj[2], aj[RR][2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                v[0][h] = load_bf16x8(x[h], chunks * 64 + chunk * 8, g.K);
+                xj[h] = load_bf16x8(x + xo[h], chunks * 64 + chunk * 8, g.K);
 #pragma unroll
-                for (int q = 0; q < RR; ++q) v[1 + q][h] = load_bf16x8(a[q][h], chunks * 64 + chunk * 8, g.K);
+                for (int q = 0; q < RR; ++q) aj[q][h] = load_bf16x8(a + ao[q][h], chunks * 64 + chunk * 8, g.K);
             }
-            multiply(v);
+            multiply(xj, aj);
         }
 #pragma unroll
         for (int q = 0; q < RR; ++q) part[wave][q][lane] = acc[q];

@@ -509,6 +509,8 @@ moe_status check_lora(const moe_lora* l)
     if (l->a == nullptr || l->b == nullptr) return fail(MOE_ERR_INVALID_ARG, "the adapters' a or b is NULL");
     if (l->rank > moe::kMaxLoraRank)
         return fail(MOE_ERR_UNSUPPORTED_SHAPE, "rank (%d) above %d is not compiled", l->rank, moe::kMaxLoraRank);
+    if (l->in_features > moe::kMaxLoraDepth)
+        return fail(MOE_ERR_UNSUPPORTED_SHAPE, "in_features (%d) above %d", l->in_features, moe::kMaxLoraDepth);
     if (l->num_adapters > moe::kMaxAdapters)
         return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%d adapters, above %d", l->num_adapters, moe::kMaxAdapters);
     if (!aligned16(l->a) || !aligned16(l->b))

@@ -82,7 +82,7 @@ def _lora(moe, **k):
 
 
 BAD_LORA = [(dict(L=0), -1), (dict(r=0), -1), (dict(K=0), -1), (dict(N=0), -1), (dict(L=-1), -1), (dict(a=None), -1),
-            (dict(b=None), -1), (dict(r=129), -2), (dict(L=65536), -2), (dict(a=A + 2), -3), (dict(b=B + 8), -3),
+            (dict(b=None), -1), (dict(r=129), -2), (dict(L=65536), -2), (dict(K=(1 << 24) + 1), -2), (dict(a=A + 2), -3), (dict(b=B + 8), -3),
             (dict(s=C + 2), -3)]
 
 
