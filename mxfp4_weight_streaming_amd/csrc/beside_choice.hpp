@@ -55,7 +55,15 @@ constexpr int lora_padded(int r) { return (r + 31) / 32 * 32; }   // ranks of a 
 // tokens takes its adapters in turn; of two requests 12.7 against 10.0.  512 of
 // rank 16: 10.4 against 25.3, and 10.3 against 9.5.
 constexpr int64_t kLoraFewValues = 16384;   // tokens times their padded rank
-constexpr int64_t kLoraFusedWork = 65536;   // values of an adapter's A
+
+// Of these, u by each workgroup itself (FUSED) saves a launch where it is little
+// work: 16 ranks or less, of a K that is walked in few steps (one token, rank 16,
+// K 2,560: 3.7 us against 5.4, 8,192: 7.7 against 9.0; rank 64, K 512: 9.8
+// against 6.2), and where most workgroups run at once (one step: 32 tokens of
+// 2,560 channels 4.8 us against 5.4, 64 5.8 against 5.6; two steps, 4,096
+// channels: 16 tokens 5.4 against 6.7 at 2,560, 32 tokens 7.5 against 6.9).
+constexpr int kLoraStep = 2560;             // values of K that a wave asks for at once
+constexpr int64_t kLoraFusedDepth = 8192;
 
 struct LoraPlan {
     bool few, fused;
@@ -76,7 +84,7 @@ constexpr LoraPlan lora_plan(int64_t M, int64_t N, int64_t K, int r)
     LoraPlan p{};
     const int64_t tn = ceil_div(N, 256), tm = ceil_div(M, 16);
     p.few = M * lora_padded(r) <= kLoraFewValues;
-    p.fused = p.few && K >= 8 && r * K <= kLoraFusedWork && M * tn <= kCus;
+    p.fused = p.few && r <= 16 && K >= 8 && K <= kLoraFusedDepth && M * tn <= (K <= kLoraStep ? 2 : 1) * kCus;
     p.shrink_slots = lora_slots(tm * ceil_div(r, r > 16 ? 32 : 16), kCus);
     p.expand_slots = lora_slots(tm * tn, 4 * kCus);
     return p;

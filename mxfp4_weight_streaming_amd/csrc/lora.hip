@@ -56,11 +56,12 @@ hipError_t expand(const LoraArgs& a, const LoraPlan& p, hipStream_t s)
 template <bool BASE32, bool F32, bool FUSED>
 hipError_t few(const LoraArgs& a, hipStream_t s)
 {
+    // (FUSED calls have 16 ranks at most)
     const auto kernel = a.r <= 8    ? lora_few_kernel<BASE32, F32, FUSED, 1>
                         : a.r <= 16 ? lora_few_kernel<BASE32, F32, FUSED, 2>
-                        : a.r <= 32 ? lora_few_kernel<BASE32, F32, FUSED, 4>
-                        : a.r <= 64 ? lora_few_kernel<BASE32, F32, FUSED, 8>
-                                    : lora_few_kernel<BASE32, F32, FUSED, 16>;
+                        : a.r <= 32 ? lora_few_kernel<BASE32, F32, false, 4>
+                        : a.r <= 64 ? lora_few_kernel<BASE32, F32, false, 8>
+                                    : lora_few_kernel<BASE32, F32, false, 16>;
     hipLaunchKernelGGL(kernel, dim3((unsigned)(a.M * ceil_div(a.N, 256))), dim3(256), 0, s, a);
     return hipGetLastError();
 }

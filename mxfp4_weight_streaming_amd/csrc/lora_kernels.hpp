@@ -18,6 +18,7 @@
 #pragma once
 
 #include "around_common.hpp"
+#include "beside_choice.hpp"
 
 namespace moe {
 
@@ -273,8 +274,7 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs g)
 // all lanes along them, so that few tokens of many adapters read each adapter
 // once and nothing else.
 // ---------------------------------------------------------------------------
-constexpr int kDotRows = 4, kDotLoads = 5;               // rows, and loads of each in flight
-constexpr int kDotStep = 512 * kDotLoads;                // values of K a wave asks for at once
+constexpr int kDotRows = 4, kDotLoads = kLoraStep / 512;   // rows, and loads of each in flight
 
 struct DotLoads {
     u32x4 x[kDotLoads], a[kDotRows][kDotLoads];
@@ -299,7 +299,7 @@ __device__ __forceinline__ void dot_load(const LoraArgs& g, int i, int64_t m, in
 template <bool SHORT>
 __device__ __forceinline__ void dot_add(const LoraArgs& g, int k0, DotLoads& v, float (&acc)[kDotRows])
 {
-    if (!SHORT && k0 + kDotStep > g.K)
+    if (!SHORT && k0 + kLoraStep > g.K)
 #pragma unroll
         for (int c = 0; c < kDotLoads; ++c)
             v.x[c] = drop_first(v.x[c], max(k0 + (c * 64 + (int)(threadIdx.x & 63)) * 8 - (g.K - 8), 0));
@@ -322,7 +322,7 @@ template <bool SHORT>
 __device__ __forceinline__ f32x4 dot_rows(const LoraArgs& g, int i, int64_t m, int r0)
 {
     float acc[kDotRows] = {};
-    for (int k0 = 0; k0 < g.K; k0 += kDotStep) {
+    for (int k0 = 0; k0 < g.K; k0 += kLoraStep) {
         DotLoads v;
         dot_load<SHORT>(g, i, m, r0, k0, v);
         dot_add<SHORT>(g, k0, v, acc);
@@ -532,18 +532,18 @@ __global__ __launch_bounds__(256) void lora_few_kernel(LoraArgs g)
             bv[s] = L > 1 ? *reinterpret_cast<const u32x4_half*>(b + first) : load_bf16x8(b, 0, g.r);
         }
         if constexpr (FUSED) {                           // (K is 8 or more)
-            auto put = [&](int r0, f32x4 u) {
-                if (lane < 4 && r0 + lane < g.r) us[r0 + lane] = lane == 0 ? u[0] : lane == 1 ? u[1] : lane == 2 ? u[2] : u[3];
-            };
-            if (g.r <= 16 && g.K <= kDotStep) {          // all at once: a loop would first wait for what is in flight
+            const int r0 = wave * 4;                     // (and r is 16 at most)
+            f32x4 u = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (g.K <= kLoraStep) {                      // all at once: a loop would first wait for what is in flight
                 DotLoads v;
                 float acc[kDotRows] = {};
-                dot_load<false>(g, i, m, wave * 4, 0, v);
+                dot_load<false>(g, i, m, r0, 0, v);
                 dot_add<false>(g, 0, v, acc);
-                put(wave * 4, dot_sum(g, i, acc));
+                u = dot_sum(g, i, acc);
             } else {
-                for (int r0 = wave * 4; r0 < g.r; r0 += 16) put(r0, dot_rows<false>(g, i, m, r0));
+                u = dot_rows<false>(g, i, m, r0);
             }
+            if (lane < 4 && r0 + lane < g.r) us[r0 + lane] = lane == 0 ? u[0] : lane == 1 ? u[1] : lane == 2 ? u[2] : u[3];
         } else {
             for (int q = threadIdx.x; q < g.r; q += 256) us[q] = g.u[m * g.rp + place_of(q, g.r)];
         }
