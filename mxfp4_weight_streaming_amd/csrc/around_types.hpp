@@ -83,8 +83,10 @@ struct LoraArgs {
     void* out;               // [M, N]
     float* u;                // [M, rp], workspace
     int64_t M, N;
-    int K, r, rp, L, base_type, out_type;   // rp: r up to a multiple of 32
-    int slots;               // by the launcher: workgroups that share a tile's adapters
+    int K, r, rp, L, out_type;   // rp: r up to a multiple of 32
+    // by the launcher
+    int slots;               // workgroups that share a tile's adapters
+    bool near;               // workgroups of the same channels on one XCD
 };
 
 }  // namespace moe

@@ -50,11 +50,23 @@ constexpr LogprobPlan logprob_plan(int64_t M, int V)
 // ---- adapters ------------------------------------------------------------------
 constexpr int lora_padded(int r) { return (r + 31) / 32 * 32; }   // ranks of a row of u
 
-// Few tokens: each reads its adapter by itself.  256 tokens of rank 64, each of
-// another adapter: 15.9 us against 29.2 on the matrix cores, where a tile of 16
-// tokens takes its adapters in turn; of two requests 12.7 against 10.0.  512 of
-// rank 16: 10.4 against 25.3, and 10.3 against 9.5.
-constexpr int64_t kLoraFewValues = 16384;   // tokens times their padded rank
+// Few tokens: each reads its adapter by itself, where the tokens' ranks are few
+// and what all of them read from the caches is at most some 100 MB.  On the
+// matrix cores tokens of one adapter share its rows, but a tile of 16 tokens takes
+// its adapters in turn.  K = N = 2,560, rank 16, us of few tokens / matrix cores:
+//   tokens        64          128         256         512         1,024
+//   an adapter    5.6 /  8.2  6.2 /  8.0  7.4 /  8.1 10.3 /  8.6  15.8 /  9.5
+//   one for 16    5.7 /  8.2  6.2 /  8.6  7.3 /  9.5 12.0 / 11.3  19.5 / 14.4
+//   one each      5.7 / 11.4  6.2 / 14.5 11.4 / 18.3 13.4 / 26.3  19.1 / 40.3
+// and 117 tokens of rank 64, 6,863 features and 8,388 channels (228 MB) 25 / 15.
+constexpr int64_t kLoraFewValues = 16384;      // tokens times their padded rank
+constexpr int64_t kLoraFewReads = 48 << 20;    // values of A and B
+
+// Few tokens' workgroups of the same channels on one XCD, so that tokens of one
+// adapter find B in its cache: 8 tokens of one adapter, rank 16, 157,184 channels
+// 9.6 us against 13.5; not where B is small (64 tokens, 2,560 channels: 5.9
+// against 5.6).
+constexpr int64_t kLoraNearTiles = 32;         // of 256 channels
 
 // Of these, u by each workgroup itself (FUSED) saves a launch where it is little
 // work: 16 ranks or less, of a K that is walked in few steps (one token, rank 16,
@@ -66,7 +78,7 @@ constexpr int kLoraStep = 2560;             // values of K that a wave asks for 
 constexpr int64_t kLoraFusedDepth = 8192;
 
 struct LoraPlan {
-    bool few, fused;
+    bool few, fused, near;
     int shrink_slots, expand_slots;
 };
 
@@ -83,7 +95,8 @@ constexpr LoraPlan lora_plan(int64_t M, int64_t N, int64_t K, int r)
 {
     LoraPlan p{};
     const int64_t tn = ceil_div(N, 256), tm = ceil_div(M, 16);
-    p.few = M * lora_padded(r) <= kLoraFewValues;
+    p.few = M * lora_padded(r) <= kLoraFewValues && M * r * (K + N) <= kLoraFewReads;
+    p.near = tn >= kLoraNearTiles;
     p.fused = p.few && r <= 16 && K >= 8 && K <= kLoraFusedDepth && M * tn <= (K <= kLoraStep ? 2 : 1) * kCus;
     p.shrink_slots = lora_slots(tm * ceil_div(r, r > 16 ? 32 : 16), kCus);
     p.expand_slots = lora_slots(tm * tn, 4 * kCus);

@@ -54,8 +54,9 @@ hipError_t expand(const LoraArgs& a, const LoraPlan& p, hipStream_t s)
 }
 
 template <bool BASE32, bool F32, bool FUSED>
-hipError_t few(const LoraArgs& a, hipStream_t s)
+hipError_t few(LoraArgs a, const LoraPlan& p, hipStream_t s)
 {
+    a.near = p.near;
     // (FUSED calls have 16 ranks at most)
     const auto kernel = a.r <= 8    ? lora_few_kernel<BASE32, F32, FUSED, 1>
                         : a.r <= 16 ? lora_few_kernel<BASE32, F32, FUSED, 2>
@@ -83,10 +84,10 @@ template <bool BASE32, bool F32>
 hipError_t add(const LoraArgs& a, hipStream_t s)
 {
     const LoraPlan p = lora_plan(a.M, a.N, a.K, a.r);
-    if (p.fused) return few<BASE32, F32, true>(a, s);
+    if (p.fused) return few<BASE32, F32, true>(a, p, s);
     const hipError_t e = shrink(a, p, s);
     if (e != hipSuccess) return e;
-    return p.few ? few<BASE32, F32, false>(a, s) : expand<BASE32, F32>(a, p, s);
+    return p.few ? few<BASE32, F32, false>(a, p, s) : expand<BASE32, F32>(a, p, s);
 }
 
 }  // namespace

@@ -506,7 +506,8 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs g)
 // a wave's load is one piece of memory (a thread a row is 64 pieces: 63 tokens of
 // rank 118 and 11,708 channels 48 us); L loads give each lane one channel, number
 // (64 / L) (lane % L) + lane / L.  A row's last values are read with those before
-// them, which count once.  FUSED: every workgroup computes its token's u itself
+// them, which count once.  Workgroups of the same channels follow one another, on
+// one XCD where B is large (near).  FUSED: every workgroup computes its token's u itself
 // (A comes from L2 after the first), which saves a launch.
 // ---------------------------------------------------------------------------
 template <bool BASE32, bool F32, bool FUSED, int L>
@@ -515,7 +516,8 @@ __global__ __launch_bounds__(256) void lora_few_kernel(LoraArgs g)
     __shared__ float us[kMaxLoraRank];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int part = lane % L, group = lane / L;
-    const int64_t m = blockIdx.x % g.M, n0 = blockIdx.x / g.M * 256 + wave * 64, n = n0 + part * (64 / L) + group;
+    const uint32_t M = (uint32_t)g.M, tile = g.near ? tile_of(blockIdx.x, gridDim.x) : blockIdx.x;
+    const int64_t m = tile % M, n0 = (int64_t)(tile / M) * 256 + wave * 64, n = n0 + part * (64 / L) + group;
     const int i = __builtin_amdgcn_readfirstlane(adapter_of(g, m));
     const size_t at = (size_t)m * g.N + min(n, g.N - 1);
     // (asked for in any case, so that it is not waited for behind a branch)

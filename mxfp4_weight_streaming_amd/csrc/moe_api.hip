@@ -523,7 +523,7 @@ moe::LoraArgs lora_args(const moe_lora* l, int32_t M, const uint16_t* x, const i
                         int32_t out_type, void* ws)
 {
     return {x, l->a, l->b, l->scale, ids, base, out, static_cast<float*>(ws), M, l->out_features, l->in_features, l->rank,
-            moe::lora_padded(l->rank), l->num_adapters, out_type, out_type, 1};
+            moe::lora_padded(l->rank), l->num_adapters, out_type, 1, false};
 }
 
 #define CHECK_ALIGN4(p)                                                                        \

@@ -65,7 +65,7 @@ def test_adapter_plans(choose):
     for (M, N, K, r), (few, fused, shrink, expand, rows) in zip(sizes, choose("lora", sizes)):
         assert shrink in (1, 2, 4, 8, 16) and expand in (1, 2, 4, 8, 16)
         assert not fused or (few and K >= 8 and r <= 16)
-        assert few == (M * (-(-r // 32) * 32) <= 16384)
+        assert few == (M * (-(-r // 32) * 32) <= 16384 and M * r * (K + N) <= 48 << 20)
         assert rows >= 256 and rows % 256 == 0 and (rows == 256 or rows * N <= 1 << 26)
 
 
