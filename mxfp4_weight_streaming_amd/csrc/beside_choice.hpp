@@ -12,13 +12,23 @@
 namespace moe {
 
 // ---- log probabilities -----------------------------------------------------------
-// Each wave walks a row 1,024 logits at a time.  Rows of at most 1,024 have a
-// wave each; others a workgroup of 256, 512 or 1,024 threads, the most with
-// which all rows' waves are resident at once, 16 a compute unit; and where rows are too few for that, they are
-// split into parts of 256 threads, joined by a second kernel.
+// Each wave walks a row 1,024 logits at a time.  Short rows have a wave each (two
+// with alternatives), others a workgroup of 256, 512 or 1,024 threads, the most
+// with which all rows' waves are resident at once, 16 a compute unit; where long
+// rows are too few for that, they are split into parts of 256 threads, joined by
+// a second kernel.  Short: a wave or two a row / a workgroup, fp32, 5
+// alternatives, us:
+//   logits          2,048        4,096        6,000        8,192
+//   16 rows        6.0 /  8.4   8.6 /  8.5  11.2 /  9.3  12.4 /  8.9
+//   512            6.3 /  9.7   9.0 / 10.0  12.5 / 11.6  13.4 / 11.3
+//   1,024          6.9 / 11.8   9.9 / 12.1  14.5 / 16.3  15.2 / 18.1
+//   4,096         16.5 / 38.4  26.4 / 41.3  39.4 / 51.5  55.0 / 51.2
+constexpr bool logprob_short(int64_t M, int V) { return V <= 2048 || (V <= 4096 && M >= 512) || (V <= 6144 && M >= 1024); }
+
 constexpr int kLogprobMaxParts = 64;            // one lane each where they are joined
-constexpr int kLogprobJoin = 1024;              // threads that join a row (one of 157,184, 20 alternatives: 256 11.5 us, 512 10.4, 1,024 10.1)
-constexpr int kLogprobShort = 1024;
+// Threads that join a row (one of 157,184, 20 alternatives: 256 11.5 us, 512
+// 10.4, 1,024 10.1).
+constexpr int kLogprobJoin = 1024;
 constexpr int64_t kLogprobWaves = 16 * kCus;
 constexpr int64_t kLogprobSplitRows = 128;      // more rows than this are not split
 
@@ -31,7 +41,8 @@ constexpr LogprobPlan logprob_plan(int64_t M, int V)
     LogprobPlan p{};
     p.threads = 64;
     p.parts = 1;
-    if (V <= kLogprobShort) return p;
+    p.segments = (int)ceil_div(V, 1024);
+    if (logprob_short(M, V)) return p;
     const bool split = M <= kLogprobSplitRows && V > 16 * 1024;
     p.threads = 256;
     // (no more waves than there are segments for)

@@ -195,10 +195,15 @@ struct LogitWalk {
 #pragma unroll
             for (int u = 0; u < Logits16<F32>::kVecs; ++u) {
                 const int p = at + (u * 64 + lane) * E;
-                x.v[u] = shift_down(x.v[u], min(max(p - (V - E), 0), E) * 8 * B);
+                if (at + u * 64 * E < V) {
+                    x.v[u] = shift_down(x.v[u], min(max(p - (V - E), 0), E) * 8 * B);
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    if (p + e >= V) x.clear(u * E + e);
+                    for (int e = 0; e < E; ++e)
+                        if (p + e >= V) x.clear(u * E + e);
+                } else {
+                    x.v[u] = F32 ? u32x4{0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u}
+                                 : u32x4{0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u};
+                }
             }
         } else {
 #pragma unroll
@@ -284,6 +289,8 @@ struct LogitWalk {
             } else {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
+                    constexpr int E = Logits16<F32>::kVec;
+                    if (at + i / E * (64 * E) >= V) break;
                     const int p = at + logit_place<F32>(lane, i);
                     ahead += __popcll(__ballot(p < V && logit_before(logit_value(x[i]), p, mine, token)));
                 }
@@ -613,74 +620,141 @@ __global__ __launch_bounds__(kLogprobJoin) void logprob_join_kernel(LogprobArgs 
     finish_row<F32, T, 256>(g, m, a, largest, (n + T - 1) / T, lds, [&] { return join_sums(mine); });
 }
 
-// A wave a row of at most 1,024 logits: they stay in its registers, and its
-// lanes' maxima bound the alternatives.
-template <bool F32>
+// A wave a row.  Where alternatives are asked for, a second wave finds them
+// meanwhile, in two passes over the same row: one after the other they are two
+// chains of thousands of cycles.  ONE: a row of at most 1,024 logits.
+template <bool F32, bool ONE>
 __global__ __launch_bounds__(256, 4) void logprob_short_kernel(LogprobArgs g)
 {
-    __shared__ uint32_t bests[4][64];
-    __shared__ alignas(16) uint64_t cands[4][kLogprobShortList];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr int E = Logits16<F32>::kVec;
+    __shared__ uint32_t bests[2][64];
+    __shared__ alignas(16) uint64_t cands[2][kLogprobShortList];
+    __shared__ double log_sums[2];
+    __shared__ float maxima[2];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), K = g.topk;
     const float inf = __builtin_inff();
-    const int64_t m = (int64_t)blockIdx.x * 4 + wave;
-    if (m >= g.M) return;
+    const int slot = K > 0 ? wave >> 1 : wave;
+    const int64_t m = (int64_t)blockIdx.x * (K > 0 ? 2 : 4) + slot;
+    const bool row = m < g.M, alternatives = K > 0 && (wave & 1) != 0;
     LogitWalk<F32> w;
-    w.row = row_of<F32>(g, m);
-    w.V = g.V;
-    w.lane = lane;
-    Logits16<F32> raw;
-    w.load(0, raw);
-    const Asked a = asked_of<F32>(g, m, w.row);
-    w.token = a.token;
-    w.asked = g.rank != nullptr && a.inside;
-    w.mine = a.mine;
-    w.above = nextafterf(w.mine, inf);
-    const float best = w.add(0, raw);
-    const RowSums r = w.sums();
-    const double log_s = finish_sums(g, m, r, a);
-    const int K = g.topk;
-    if (K == 0) return;
-    auto put = [&](int k, float x, int i) {
-        g.topk_ids[m * K + k] = i;
-        g.topk_logprob[m * K + k] = i < 0 ? -inf : log_p(x, r.m, log_s);
-    };
-    bests[wave][lane] = lane_order(best);
-#pragma unroll
-    for (int c = 0; c < kLogprobShortList; c += 64) cands[wave][c + lane] = 0;
-    __builtin_amdgcn_wave_barrier();
-    const float bound = kth_bound(bests[wave][lane], bests[wave], K);
-    int n = 0;
-    uint64_t keys[16];                                   // 0: not a candidate
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float x = logit_value(raw.get(i));
-        const int p = logit_place<F32>(lane, i);
-        const bool in = p < g.V && x >= bound && x > -inf;
-        keys[i] = in ? (uint64_t)float_order(x) << 32 | (uint32_t)~p : 0;
-        const uint64_t who = __ballot(in);
-        const int at = n + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
-        if (in && at < kLogprobShortList) cands[wave][at] = keys[i];
-        n += __popcll(who);
+    if (row) {
+        w.row = row_of<F32>(g, m);
+        w.V = g.V;
+        w.lane = lane;
     }
-    __builtin_amdgcn_wave_barrier();
-    if (n <= kLogprobShortList) {
-        for (int c = lane; c < n; c += 64) {
-            const uint64_t own = cands[wave][c];
-            const int at = key_place(cands[wave], n, own);
-            if (at < K) put(at, order_float((uint32_t)(own >> 32)), (int)~(uint32_t)own);
+    if (row && !alternatives) {
+        Logits16<F32> now, next;
+        w.load(0, now);
+        const Asked a = asked_of<F32>(g, m, w.row);
+        w.token = a.token;
+        w.asked = g.rank != nullptr && a.inside;
+        w.mine = a.mine;
+        w.above = nextafterf(w.mine, inf);
+        if constexpr (ONE) {
+            w.add(0, now);
+        } else {
+#pragma unroll 1
+            for (int at = 0; at < g.V; at += 1024) {
+                if (at + 1024 < g.V) w.load(at + 1024, next);
+                w.add(at, now);
+                now = next;
+            }
         }
-        for (int k = n + lane; k < K; k += 64) put(k, -inf, -1);
+        const RowSums r = w.sums();
+        const double log_s = finish_sums(g, m, r, a);
+        if (K > 0 && lane == 0) {
+            log_sums[slot] = log_s;
+            maxima[slot] = r.m;
+        }
+    }
+    if (K == 0) return;
+    Logits16<F32> raw, next;
+    int n = 0, place[kLogprobShortList / 64];
+    uint64_t own[kLogprobShortList / 64];
+    auto key_of = [&](int at, int i) {                   // 0: no logit, or nothing above -inf
+        const float x = logit_value(raw.get(i));
+        const int p = at + logit_place<F32>(lane, i);
+        return p < g.V && x > -inf ? (uint64_t)float_order(x) << 32 | (uint32_t)~p : 0ull;
+    };
+    // f of 1,024 logits at a time
+    auto each = [&](auto f) {
+        if constexpr (ONE) {
+            f(0);
+        } else {
+            w.load(0, raw);
+#pragma unroll 1
+            for (int at = 0; at < g.V; at += 1024) {
+                if (at + 1024 < g.V) w.load(at + 1024, next);
+                f(at);
+                raw = next;
+            }
+        }
+    };
+    if (row && alternatives) {
+        if constexpr (ONE) w.load(0, raw);
+        float best = -inf;
+        each([&](int) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) best = fmaxf(best, logit_value(raw.get(i)));   // (behind the row: -inf)
+        });
+        bests[slot][lane] = lane_order(best);
+#pragma unroll
+        for (int c = 0; c < kLogprobShortList; c += 64) cands[slot][c + lane] = 0;
+        __builtin_amdgcn_wave_barrier();
+        const float bound = kth_bound(bests[slot][lane], bests[slot], K);
+        const uint64_t least = bound > -inf ? (uint64_t)float_order(bound) << 32 : 1;
+        each([&](int at) {
+#pragma unroll
+            for (int u = 0; u < 16; u += E) {
+                if (at + u * 64 >= g.V) break;                // (u of 16 values of a lane: 64 u of the wave's)
+#pragma unroll
+                for (int i = u; i < u + E; ++i) {
+                    const uint64_t key = key_of(at, i);
+                    const uint64_t who = __ballot(key >= least);
+                    if (who == 0) continue;
+                    const int to = n + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
+                    if (key >= least && to < kLogprobShortList) cands[slot][to] = key;
+                    n += __popcll(who);
+                }
+            }
+        });
+        __builtin_amdgcn_wave_barrier();
+        if (n <= kLogprobShortList)
+#pragma unroll
+            for (int c = 0; c < kLogprobShortList / 64; ++c) {
+                own[c] = cands[slot][c * 64 + lane];
+                place[c] = c * 64 < n ? key_place(cands[slot], n, own[c]) : K;
+            }
+    }
+    __syncthreads();
+    if (!row || !alternatives) return;
+    const double log_s = log_sums[slot];
+    const float row_m = maxima[slot];
+    auto put = [&](int k, uint64_t key) {
+        const bool none = key == 0;
+        g.topk_ids[m * K + k] = none ? -1 : (int)~(uint32_t)key;
+        g.topk_logprob[m * K + k] = none ? -inf : log_p(order_float((uint32_t)(key >> 32)), row_m, log_s);
+    };
+    if (n <= kLogprobShortList) {
+#pragma unroll
+        for (int c = 0; c < kLogprobShortList / 64; ++c)
+            if (c * 64 + lane < n && place[c] < K) put(place[c], own[c]);
+        for (int k = n + lane; k < K; k += 64) put(k, 0);
         return;
     }
-    // (equal logits) the largest key left, K times
+    // (equal logits) the largest key below the last, K times
+    uint64_t last = ~0ull;
     for (int k = 0; k < K; ++k) {
         uint64_t top = 0;
+        each([&](int at) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) top = max_u64(top, keys[i]);
-        top = wave_max_u64(top);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) keys[i] = keys[i] == top ? 0 : keys[i];
-        if (lane == 0) put(k, order_float((uint32_t)(top >> 32)), (int)~(uint32_t)top);
+            for (int i = 0; i < 16; ++i) {
+                const uint64_t key = key_of(at, i);
+                if (key < last) top = max_u64(top, key);
+            }
+        });
+        last = wave_max_u64(top);
+        if (lane == 0) put(k, last);
     }
 }
 

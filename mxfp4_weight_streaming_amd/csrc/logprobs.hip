@@ -50,9 +50,10 @@ hipError_t launch(LogprobArgs a, hipStream_t s)
     a.parts = p.parts;
     a.part_segments = p.part_segments;
     if (p.threads == 64) {
-        const int64_t grid = ceil_div(a.M, 4);
+        const int64_t grid = ceil_div(a.M, a.topk > 0 ? 2 : 4);
         if (grid * 256 > 0xFFFFFFFFll) return hipErrorInvalidConfiguration;   // beyond a launch's threads
-        hipLaunchKernelGGL((logprob_short_kernel<F32>), dim3((unsigned)grid), dim3(256), 0, s, a);
+        const auto kernel = p.segments == 1 ? logprob_short_kernel<F32, true> : logprob_short_kernel<F32, false>;
+        hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(256), 0, s, a);
         return hipGetLastError();
     }
     if (p.parts == 1) return p.threads == 256 ? rows<F32, 256>(a, s) : p.threads == 512 ? rows<F32, 512>(a, s) : rows<F32, 1024>(a, s);
