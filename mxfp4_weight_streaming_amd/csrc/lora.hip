@@ -40,8 +40,7 @@ hipError_t expand_tiles(LoraArgs a, const LoraPlan& p, hipStream_t s)
     a.slots = p.expand_slots;
     const int64_t grid = expand_grid(a, p);
     const auto kernel = lora_expand_kernel<BASE32, F32, RK, SHORT>;
-    const uint32_t lds = 3 * 16 * (a.rp / 2 + 4) * 4;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(256), lds, s, a);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 

@@ -407,13 +407,20 @@ __device__ __forceinline__ void store_row4(void* p, size_t at, int n, const floa
     }
 }
 
+// Where 16 bytes c of a row of 4 RK of them stand, so that the lanes that LDS
+// serves together, 16 rows' operands, meet no bank twice.
+template <int RK>
+__device__ __forceinline__ int swizzled(int row, int c)
+{
+    return row * 4 * RK + (c ^ (RK == 1 ? row >> 1 & 3 : RK == 2 ? row & 7 : row));
+}
+
 template <bool BASE32, bool F32, int RK, bool SHORT>
 __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs g)
 {
-    __shared__ u32x4 stage[4][4 * RK][64];
-    extern __shared__ uint32_t us[];                     // [3][16][rp / 2 + 4]
+    __shared__ u32x4 stage[4][4 * RK][64], us[3][16 * 4 * RK];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int row = lane & 15, quarter = lane >> 4, stride = g.rp / 2 + 4;
+    const int row = lane & 15, quarter = lane >> 4;
     const uint32_t tn = (uint32_t)((g.N + 255) / 256), tiles = (uint32_t)((g.M + 15) / 16) * tn;
     const uint32_t slot = blockIdx.x / tiles, tile = tile_of(blockIdx.x - slot * tiles, tiles);
     const int64_t m0 = (int64_t)(tile / tn) * 16, n0 = (int64_t)(tile % tn) * 256 + wave * 64, n = n0 + row * 4;
@@ -458,7 +465,7 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs g)
         if (q >= 16 * quads) break;
         const Split3 lo = split_pair(uq[i][0], uq[i][1]), hi = split_pair(uq[i][2], uq[i][3]);
 #pragma unroll
-        for (int p = 0; p < 3; ++p) *reinterpret_cast<u32x2*>(us + (p * 16 + t) * stride + 2 * c) = u32x2{lo.v[p], hi.v[p]};
+        for (int p = 0; p < 3; ++p) reinterpret_cast<u32x2*>(&us[p][swizzled<RK>(t, c >> 1)])[c & 1] = u32x2{lo.v[p], hi.v[p]};
     }
     lds_barrier();
     float o[4][4];
@@ -475,17 +482,17 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs g)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int k = 0; k < RK; ++k) stage[wave][j * RK + k][lane ^ ((lane >> 3) & 3)] = bv[j][k];
+            for (int k = 0; k < RK; ++k) stage[wave][j * RK + k][swizzled<1>(lane >> 2, lane & 3)] = bv[j][k];
 #pragma unroll
         for (int k = 0; k < RK; ++k) {
             if (k * 32 >= g.rp) break;                   // (ranks 65 to 96)
             u32x4 bw[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) bw[j] = stage[wave][j * RK + k][row * 4 + (quarter ^ ((row >> 1) & 3))];
+            for (int j = 0; j < 4; ++j) bw[j] = stage[wave][j * RK + k][swizzled<1>(row, quarter)];
 #pragma unroll
             for (int p = 2; p >= 0; --p) {
                 // (a token of another adapter has its own u here, and drops the result)
-                const u32x4 uv = *reinterpret_cast<const u32x4*>(us + (p * 16 + row) * stride + 16 * k + quarter * 4);
+                const u32x4 uv = us[p][swizzled<RK>(row, 4 * k + quarter)];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc[j] = mfma(uv, bw[j], acc[j]);
             }
