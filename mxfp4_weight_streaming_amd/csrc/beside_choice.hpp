@@ -12,12 +12,8 @@
 namespace moe {
 
 // ---- log probabilities -----------------------------------------------------------
-// Each wave walks a row 1,024 logits at a time.  Short rows have a wave each (two
-// with alternatives), others a workgroup of 256, 512 or 1,024 threads, the most
-// with which all rows' waves are resident at once, 16 a compute unit; where long
-// rows are too few for that, they are split into parts of 256 threads, joined by
-// a second kernel.  Short: a wave or two a row / a workgroup, fp32, 5
-// alternatives, us:
+// Each wave walks a row 1,024 logits at a time.  Short rows have a wave or, with
+// alternatives, two each.  Against a workgroup a row, fp32, 5 alternatives, us:
 //   logits          2,048        4,096        6,000        8,192
 //   16 rows        6.0 /  8.4   8.6 /  8.5  11.2 /  9.3  12.4 /  8.9
 //   512            6.3 /  9.7   9.0 / 10.0  12.5 / 11.6  13.4 / 11.3
@@ -25,12 +21,25 @@ namespace moe {
 //   4,096         16.5 / 38.4  26.4 / 41.3  39.4 / 51.5  55.0 / 51.2
 constexpr bool logprob_short(int64_t M, int V) { return V <= 2048 || (V <= 4096 && M >= 512) || (V <= 6144 && M >= 1024); }
 
+// Other rows have a workgroup of 256, 512 or 1,024 threads each, the most with
+// which all rows' waves are resident at once, 16 a compute unit (32,768 logits,
+// 256 / 512 / 1,024 threads: 256 rows 19.8 / 15.6 / 16.9 us, 512 22.9 / 22.1 /
+// 30.7, 1,024 31.7 / 37.8 / 55.6).
+constexpr int64_t kLogprobWaves = 16 * kCus;
+
+// Few long rows are split into parts of 256 threads, joined by a second kernel:
+// split / a workgroup a row, us:
+//   rows             4            64           128          256
+//   8,192 logits    9.3 /  8.4   9.9 /  8.8  10.2 /  8.8  10.8 /  9.0
+//   20,000          9.4 / 10.2  10.6 / 11.1  11.4 / 11.3  13.9 / 12.1
+//   157,184         9.9 / 25.3  19.4 / 28.8  26.3 / 29.7  38.4 / 35.3
+constexpr int64_t kLogprobSplitRows = 128;
+constexpr int kLogprobSplitLogits = 16 * 1024;
+constexpr int64_t kLogprobSplit = 1024;         // workgroups in all
 constexpr int kLogprobMaxParts = 64;            // one lane each where they are joined
 // Threads that join a row (one of 157,184, 20 alternatives: 256 11.5 us, 512
 // 10.4, 1,024 10.1).
 constexpr int kLogprobJoin = 1024;
-constexpr int64_t kLogprobWaves = 16 * kCus;
-constexpr int64_t kLogprobSplitRows = 128;      // more rows than this are not split
 
 struct LogprobPlan {
     int threads, segments, group_segments, groups, parts, part_segments;   // threads 64: the short rows' kernel
@@ -43,7 +52,7 @@ constexpr LogprobPlan logprob_plan(int64_t M, int V)
     p.parts = 1;
     p.segments = (int)ceil_div(V, 1024);
     if (logprob_short(M, V)) return p;
-    const bool split = M <= kLogprobSplitRows && V > 16 * 1024;
+    const bool split = M <= kLogprobSplitRows && V > kLogprobSplitLogits;
     p.threads = 256;
     // (no more waves than there are segments for)
     while (!split && p.threads < 1024 && M * p.threads / 64 * 2 <= kLogprobWaves && V > 16 * p.threads) p.threads *= 2;
@@ -52,7 +61,7 @@ constexpr LogprobPlan logprob_plan(int64_t M, int V)
     // thread of one that has just been walked
     p.group_segments = (int)ceil_div(p.segments, split ? kLogprobMaxParts : 16);
     p.groups = (int)ceil_div(p.segments, p.group_segments);
-    const int64_t parts = split ? std::min<int64_t>({ceil_div(1024, M), kLogprobMaxParts, p.groups}) : 1;
+    const int64_t parts = split ? std::min<int64_t>({ceil_div(kLogprobSplit, M), kLogprobMaxParts, p.groups}) : 1;
     p.part_segments = (int)ceil_div(p.groups, parts) * p.group_segments;   // whole groups
     p.parts = (int)ceil_div(p.segments, p.part_segments);
     return p;
@@ -69,7 +78,7 @@ constexpr int lora_padded(int r) { return (r + 31) / 32 * 32; }   // ranks of a 
 //   an adapter    5.6 /  8.2  6.2 /  8.0  7.4 /  8.1 10.3 /  8.6  15.8 /  9.5
 //   one for 16    5.7 /  8.2  6.2 /  8.6  7.3 /  9.5 12.0 / 11.3  19.5 / 14.4
 //   one each      5.7 / 11.4  6.2 / 14.5 11.4 / 18.3 13.4 / 26.3  19.1 / 40.3
-// and 117 tokens of rank 64, 6,863 features and 8,388 channels (228 MB) 25 / 15.
+// and 117 tokens of rank 64, 6,863 features and 8,388 channels (228 MB) 25 / 21.
 constexpr int64_t kLoraFewValues = 16384;      // tokens times their padded rank
 constexpr int64_t kLoraFewReads = 48 << 20;    // values of A and B
 
@@ -94,7 +103,9 @@ struct LoraPlan {
 };
 
 // The adapters of a tile of 16 tokens are dealt to so many workgroups (at most
-// 16: a token each) that there is one for every compute unit.
+// 16: a token each) that there is one for every compute unit (300 tokens of 9
+// requests, rank 64: 10.1 us, the whole tile by one 16.6; 512 tokens with an
+// adapter each, rank 32: 34.7, 73.2).
 constexpr int lora_slots(int64_t tiles, int64_t target)
 {
     int slots = 1;

@@ -170,7 +170,9 @@ __device__ __forceinline__ void store_u(const LoraArgs& g, int64_t m, int k, f32
 // neighbouring lanes, which as loads are 16 lines of memory at 16 bytes each (a
 // lane a clock: 2,048 tokens of rank 64 16 us); here 8 lanes read a row's 128
 // bytes, and the operands are read back from the wave's own 2 KB of LDS a tile
-// (chunk c of row r at c ^ r % 8, so that neither side has bank conflicts).
+// (chunk c of row r at c ^ r % 8, so that neither side has bank conflicts): 8 us,
+// bound by latencies: ids, then A, then the waves' sums, with one workgroup a
+// compute unit, and by the tiles that two adapters share (3 us).  Rank 16: 5 us.
 // ---------------------------------------------------------------------------
 template <int RR>
 __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs g)
@@ -272,7 +274,8 @@ __global__ __launch_bounds__(512) void lora_shrink_kernel(LoraArgs g)
 // ---------------------------------------------------------------------------
 // u of one token and 16 rows of A, for few tokens: a wave takes 4 rows of A,
 // all lanes along them, so that few tokens of many adapters read each adapter
-// once and nothing else.
+// once and nothing else; all loads of 2,560 values are in flight at once.  64
+// tokens of rank 16, K 2,560: 2.7 us, a launch and one round of latency.
 // ---------------------------------------------------------------------------
 constexpr int kDotRows = 4, kDotLoads = kLoraStep / 512;   // rows, and loads of each in flight
 
@@ -343,12 +346,17 @@ __global__ __launch_bounds__(256) void lora_shrink_few_kernel(LoraArgs g)
 }
 
 // ---------------------------------------------------------------------------
-// out of 16 tokens and 256 channels, 64 a wave.  u's
-// three parts stand in LDS, rows padded by 16 bytes; they are the first operand
-// and B's rows the second, row q of tile j being channel 4 q + j, so that a lane
-// gets 4 consecutive channels of 4 tokens, and 16 lanes a token's 64: base and
-// out are read and written 128 bytes (bf16) a row.  (Two or four tiles of tokens in
-// turn, B's rows kept, were no faster.)  RK: steps of 32 ranks.
+// out of 16 tokens and 256 channels, 64 a wave.  u's three parts stand in LDS;
+// they are the first operand and B's rows the second, row q of tile j being
+// channel 4 q + j, so that a lane gets 4 consecutive channels of 4 tokens, and 16
+// lanes a token's 64: base and out are read and written 128 bytes (bf16) a row.
+// B's rows are loaded by 4 lanes each, 64 bytes, and dealt to the operand's lanes
+// through LDS (loaded in the operand's order, a lane a clock, 2,048 tokens of
+// rank 128 took 2 us more).  RK: steps of 32 ranks; SHORT: less than 8 ranks.
+// 2,048 tokens and 2,560 channels of bf16: rank 16 9.5 us, rank 64 11; 21 MB of
+// base and out are 4.5 us at a copy's rate, and the rest latencies (ids, B, LDS)
+// of 5 workgroups a compute unit, 4 at a time.  Two to eight tiles of tokens in
+// turn, B's rows kept, were no faster.
 // ---------------------------------------------------------------------------
 template <bool F32>
 struct Row4 {
@@ -511,11 +519,14 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs g)
 // out of one token and 256 channels, 64 a wave: for few tokens, whose lanes a
 // tile of 16 would leave idle.  L lanes share a row of B, 8 values each, so that
 // a wave's load is one piece of memory (a thread a row is 64 pieces: 63 tokens of
-// rank 118 and 11,708 channels 48 us); L loads give each lane one channel, number
-// (64 / L) (lane % L) + lane / L.  A row's last values are read with those before
-// them, which count once.  Workgroups of the same channels follow one another, on
-// one XCD where B is large (near).  FUSED: every workgroup computes its token's u itself
-// (A comes from L2 after the first), which saves a launch.
+// rank 118 and 11,708 channels 48 us, now 17); L loads give each lane one
+// channel, number (64 / L) (lane % L) + lane / L.  A row's last values are read
+// with those before them, which count once.  Workgroups of the same channels
+// follow one another, on one XCD where B is large (near).  FUSED: every workgroup
+// computes its token's u itself (A comes from L2 after the first), which saves a
+// launch: one token of rank 16, 2,560 to 2,560, 3.7 us, of which a launch is 1.6
+// and the rest ids, A and x, and the sums' reduction.  Four tokens and 157,184
+// channels, 25.5 MB: 7.3 us with the launch before it, 3.5 TB/s.
 // ---------------------------------------------------------------------------
 template <bool BASE32, bool F32, bool FUSED, int L>
 __global__ __launch_bounds__(256) void lora_few_kernel(LoraArgs g)
