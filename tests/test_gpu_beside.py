@@ -163,6 +163,24 @@ def test_two_streams_at_once(moe):
             assert np.array_equal(got[n].view(np.uint8), want[n].view(np.uint8)), n
 
 
+def test_wide_rows_in_a_graph(moe):
+    """Rows whose groups' maxima take more LDS than a kernel has by default, captured without an eager call before."""
+    g = torch.Generator().manual_seed(11)
+    M, V, k = 129, 270000, 2
+    x, t = torch.randn(M, V, generator=g), torch.randint(0, V, (M,), generator=g).to(torch.int32)
+    xd, td, o = x.cuda(), t.cuda(), [Out((M,), F32), Out((M,), torch.int32), Out((M,), F32), Out((M, k), torch.int32), Out((M, k), F32)]
+    ws, graph = moe.logprobs_workspace(M, V, k), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        moe.moe_token_logprobs(xd, td, *(v.t for v in o), ws)
+    ref = Logprobs(x, t, k)
+    for _ in range(3):
+        for v in o:
+            v.t.view(torch.uint8).fill_(0xA5)
+        graph.replay()
+        torch.cuda.synchronize()
+        ref.check(*(v.bits() for v in o))
+
+
 def test_a_large_workspace_serves_fewer_tokens(moe):
     """A workspace for many tokens serves any smaller call; what a call does not use of it stays as it was."""
     V, k = 40000, 4
