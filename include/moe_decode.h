@@ -509,9 +509,9 @@ typedef struct {
 
 /* Bytes of workspace that moe_lora_add and moe_int8_linear_lora need for up to
  * max_tokens tokens; 0 for invalid sizes.  Most of it (256 MB at most, or 256
- * rows) is the product in fp32 on its way to bf16: moe_lora_add needs only the
- * u of each token, 4 bytes a rank, ranks counted up to a multiple of 32, in all
- * up to a multiple of 256. */
+ * rows) is the product in fp32 on its way to bf16: moe_lora_add, and
+ * moe_int8_linear_lora with an fp32 out, need only the u of each token, 4 bytes a
+ * rank, ranks counted up to a multiple of 32, in all up to a multiple of 256. */
 size_t moe_lora_workspace_bytes(const moe_lora* lora, int32_t max_tokens);
 
 /* Adds each token's adapter to a projection's output.  For token m with adapter

@@ -671,8 +671,8 @@ def moe_lora_workspace_bytes(lp: MoeLora, max_tokens: int) -> int:
 
 
 def lora_workspace(lp: MoeLora, max_tokens: int, product: bool = True):
-    """A workspace (allocated through torch) for up to max_tokens tokens; for moe_lora_add alone where product is false,
-    which takes much less."""
+    """A workspace (allocated through torch) for up to max_tokens tokens.  Where product is false, one that serves
+    moe_lora_add, and moe_int8_linear_lora into float32, which takes much less."""
     import torch
     n = moe_lora_workspace_bytes(lp, max_tokens)
     if n == 0:

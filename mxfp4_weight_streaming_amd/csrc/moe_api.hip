@@ -1105,8 +1105,8 @@ moe_status moe_int8_linear_lora(const int8_t* a, const float* a_scale, const int
                     moe::kMaxInt8Depth);
     CHECK_ALIGN(a); CHECK_ALIGN(w); CHECK_ALIGN(x); CHECK_ALIGN(out);
     CHECK_ALIGN4(a_scale); CHECK_ALIGN4(w_scale); CHECK_ALIGN4(adapter_ids);
-    const size_t need = moe::lora_product_workspace(M, lora->out_features, lora->rank), L = lora->num_adapters, r = lora->rank,
-                 K = lora->in_features, N = lora->out_features;
+    const size_t L = lora->num_adapters, r = lora->rank, K = lora->in_features, N = lora->out_features,
+                 need = out_type == MOE_TYPE_F32 ? moe::lora_add_workspace(M, (int)r) : moe::lora_product_workspace(M, (int64_t)N, (int)r);
     if ((st = check_scratch(ws, ws_bytes, need, M)) != MOE_OK) return st;
     const Range in[] = {{a, (size_t)M * K, "a"},
                         {w, N * K, "w"},

@@ -71,6 +71,10 @@ def test_adding_adapters_needs_their_u_alone(moe, M, r):
     call = lambda ws, n: moe.raw().moe_lora_add(ctypes.byref(lp), M, D, E, None, G, 0, ws, n, None)  # noqa: E731
     assert call(H, need - 1) == -4 and "workspace" in moe.moe_last_error()
     assert call(D, need) == -1 and "overlap" in moe.moe_last_error()
+    # the int8 projection into fp32 as well; into bf16 it keeps its product in the workspace, too
+    call = lambda ws, n, kind: moe.raw().moe_int8_linear_lora(  # noqa: E731
+        D, E, F, G, ctypes.byref(lp), M, H, I, 1 << 48, kind, ws, n, None)
+    assert call(1 << 49, need - 1, 1) == -4 and call(1 << 48, need, 1) == -1 and call(1 << 49, need, 0) == -4
 
 
 LORA = dict(L=4, r=16, K=64, N=96, a=A, b=B, s=C)

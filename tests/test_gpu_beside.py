@@ -163,6 +163,28 @@ def test_two_streams_at_once(moe):
             assert np.array_equal(got[n].view(np.uint8), want[n].view(np.uint8)), n
 
 
+@pytest.mark.parametrize("M", [3, 40, 600])
+def test_int8_into_fp32_with_the_small_workspace(moe, M):
+    """What the header says it needs is enough, and nothing behind it is written; the same bits as with a large one."""
+    g = torch.Generator().manual_seed(M)
+    L, r, K, N = 3, 40, 96, 300
+    a, b = torch.randn(L, r, K, generator=g).to(BF).cuda(), torch.randn(L, N, r, generator=g).to(BF).cuda()
+    lp = moe.lora(a, b)
+    q, w = (torch.randint(-127, 128, s, generator=g).to(I8).cuda() for s in ((M, K), (N, K)))
+    qs, ws = torch.rand(M, generator=g).cuda(), torch.rand(N, generator=g).cuda()
+    x, ids = torch.randn(M, K, generator=g).to(BF).cuda(), torch.randint(-1, L, (M,), generator=g).to(torch.int32).cuda()
+    small = moe.lora_workspace(lp, M, product=False)
+    raw = torch.full((small.nbytes + 4096,), 0xC3, dtype=torch.uint8, device="cuda")
+    outs = [Out((M, N), F32) for _ in range(2)]
+    moe.moe_int8_linear_lora(q, qs, w, ws, lp, x, ids, outs[0].t, raw[:small.nbytes])
+    moe.moe_int8_linear_lora(q, qs, w, ws, lp, x, ids, outs[1].t, moe.lora_workspace(lp, M))
+    torch.cuda.synchronize()
+    assert bool((raw[small.nbytes:] == 0xC3).all()) and same_f32(outs[0].bits(), outs[1].bits())
+    d, err = lora_delta(x, a, b, None, ids)
+    base = (q.cpu().double() @ w.cpu().double().T) * qs.cpu().double()[:, None] * ws.cpu().double()
+    check_rows(outs[0].bits(), base + d, err + 2.0 ** -22 * base.abs(), F32)
+
+
 def test_wide_rows_in_a_graph(moe):
     """Rows whose groups' maxima take more LDS than a kernel has by default, captured without an eager call before."""
     g = torch.Generator().manual_seed(11)
