@@ -51,11 +51,12 @@ def test_logprob_plans(choose):
 
 def test_logprob_tests_reach_every_kernel(choose):
     """Sizes of tests/test_gpu_logprobs.py."""
-    sizes = [(5, 8191), (300, 5003), (1025, 1000), (2500, 130), (1, 157184), (64, 40000), (130, 262144), (130, 300007), (300, 30011),
-             (600, 20011), (128, 16400), (129, 16400), (1, 1000003)]
+    sizes = [(5, 8191), (300, 5003), (1025, 1000), (17, 2048), (512, 4096), (1024, 6144), (1, 157184), (64, 40000),
+             (130, 262144), (130, 300007), (300, 30011), (600, 20011), (128, 16400), (129, 16400), (1, 1000003)]
     got = choose("logprobs", sizes)
     kinds = {(g[0], g[4] > 1) for g in got}
     assert kinds == {(64, False), (256, False), (512, False), (1024, False), (256, True)}
+    assert {g[1] for g in got if g[0] == 64} == {1, 2, 4, 6}
     assert any(g[2] > 1 and g[4] > 1 for g in got) and any(g[2] > 1 and g[4] == 1 for g in got)   # groups of several segments
 
 
@@ -72,7 +73,9 @@ def test_adapter_plans(choose):
 def test_adapter_tests_reach_every_kernel(choose):
     """The sizes of tests/test_gpu_lora.py: fused and not, few and many, with slots and without."""
     got = choose("lora", [(1, 2560, 2560, 16), (64, 2560, 2560, 16), (9, 200, 96, 16), (1, 70, 130, 16), (300, 48, 64, 128),
-                          (512, 1024, 2560, 64), (2048, 768, 512, 16), (130, 2563, 769, 100)])
+                          (512, 1024, 2560, 64), (2048, 768, 512, 16), (130, 2563, 769, 100),
+                          (16, 60000, 256, 64), (60, 3400, 3300, 128)])
+    assert [g[0] for g in got[-2:]] == [0, 0]            # few tokens that would read too much by themselves
     assert {(g[0], g[1]) for g in got} == {(1, 1), (1, 0), (0, 0)}
     many = [g for g in got if not g[0]]
     assert any(g[2] > 1 for g in many) and any(g[3] > 1 for g in many)

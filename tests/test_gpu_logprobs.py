@@ -212,3 +212,33 @@ def test_offsets_beyond_32_bits(moe):
     rows.copy_(x)
     lp, rank, ent, ids, top = _run(moe, rows, t.cuda(), 4)
     Logprobs(x, t, 4).check(lp, rank, ent, ids, top)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [1024, 1025, 1100, 1500, 2047, 2048])
+def test_rows_of_two_segments(moe, V, dtype):
+    """Rows that a wave walks in two steps: sizes, distances, masks, ties."""
+    test_vocabularies(moe, V, dtype)
+    test_masks(moe, V, dtype)
+    test_ties_and_orders(moe, V, dtype)
+    test_rows_apart(moe, V, 3, dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,V,pad", [(512, 2049, 0), (520, 3333, 5), (512, 4096, 0), (1024, 4097, 1), (1030, 6143, 2),
+                                     (1024, 6144, 0)])
+def test_many_rows_of_some_segments(moe, M, V, pad, dtype):
+    """... and of up to six: many rows, plain ones beside flat, stepped, masked and empty ones."""
+    print(f"M={M} V={V} pad={pad} {dtype}", flush=True)
+    x, t = _logits(M + V, M, V, torch.float32)
+    ramp = torch.linspace(-8.0, 8.0, V)
+    odd = [torch.zeros(V), ramp, torch.floor(ramp), (torch.arange(V) % 64).float(), torch.full((V,), -INF), torch.full((V,), float("nan")),
+           torch.where(torch.arange(V) == V - 1, 1.0, -INF), torch.where(torch.arange(V) >= V - 2, 1.0, 0.0),
+           torch.where(torch.arange(V) % 3 == 0, float("nan"), -ramp), torch.full((V,), torch.finfo(dtype).min)]
+    for i, row in enumerate(odd):
+        for at in (i, M - 1 - i, M // 2 + i):
+            x[at] = row
+    full = torch.full((M, V + pad), INF, dtype=dtype)
+    full[:, :V] = x.to(dtype)
+    for k in (0, 3, 32):
+        _check(moe, full[:, :V], t, k)

@@ -266,3 +266,51 @@ def test_infinite_and_largest_values(moe, M, r):
     got = out.cpu().double()
     assert bool(inf[0].all()) and bool((got[inf] == torch.inf).all())
     check_rows(torch.where(inf, 0.0, got), torch.where(inf, 0.0, ref), torch.where(inf, 0.0, err), torch.float32)
+
+
+@pytest.mark.parametrize("M,L,r,K,N,dtype,kind", [
+    (9, 9, 40, 300, 9000, torch.float32, "any"), (7, 3, 64, 72, 20001, torch.bfloat16, "runs"), (2, 2, 9, 40, 140000, torch.bfloat16, "any"),
+    (16, 16, 64, 256, 60000, torch.float32, "any"), (5, 2, 128, 130, 90001, torch.bfloat16, "any"), (3, 3, 121, 64, 160003, torch.float32, "any"),
+    (60, 60, 128, 3300, 3400, torch.bfloat16, "any")])
+def test_few_tokens_of_many_channels(moe, M, L, r, K, N, dtype, kind):
+    """By themselves with the workgroups of the same channels side by side, and on the matrix cores where they would read
+    too much."""
+    _check_add(moe, M + r, M, L, r, K, N, dtype, kind)
+
+
+@pytest.mark.parametrize("M", [3, 40])
+def test_adapters_beyond_32_bits(moe, M):
+    """The last of many adapters, beyond 2^31 values of B (and, of A, of a second set)."""
+    g = torch.Generator().manual_seed(M)
+    for L, r, K, N in ((220, 64, 24, 160000), (70, 128, 262144, 40)):
+        a = torch.empty(L, r, K, dtype=torch.bfloat16, device="cuda")
+        b = torch.empty(L, N, r, dtype=torch.bfloat16, device="cuda")
+        ends = [torch.randn(2, r, K, generator=g).to(torch.bfloat16), torch.randn(2, N, r, generator=g).to(torch.bfloat16) / 8]
+        for t, v in zip((a, b), ends):
+            t[0], t[L - 1] = v[0].cuda(), v[1].cuda()
+        x = torch.randn(M, K, generator=g).to(torch.bfloat16)
+        ids = torch.where(torch.rand(M, generator=g) < 0.5, 0, L - 1).to(torch.int32)
+        ids[0], ids[M - 1] = L - 1, 0
+        out = _add(moe, a, b, None, x, ids, None, torch.float32)
+        d, err = lora_delta(x, *ends, None, (ids > 0).to(torch.int32))
+        check_rows(out, d, err, torch.float32)
+
+
+def test_outputs_beyond_32_bits(moe):
+    """Rows of out beyond 2^31 elements and 2^32 bytes, with and without the int8 projection."""
+    g = torch.Generator().manual_seed(8)
+    M, N, K, L, r = 14000, 157184, 16, 3, 8
+    a, b, _ = _adapters(g, L, r, K, N, False)
+    x, ids = torch.randn(M, K, generator=g).to(torch.bfloat16), torch.randint(-1, L, (M,), generator=g).to(torch.int32)
+    lp, rows = moe.lora(a.cuda(), b.cuda()), [0, 1, 13660, 13663, M - 2, M - 1]
+    out = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    ws = moe.lora_workspace(lp, M)
+    moe.moe_lora_add(lp, x.cuda(), ids.cuda(), None, out, ws)
+    d, err = lora_delta(x[rows], a, b, None, ids[rows])
+    check_rows(out[rows], d, err, torch.bfloat16)
+    q, w = (torch.randint(-127, 128, s, generator=g).to(torch.int8) for s in ((M, K), (N, K)))
+    qs, wsc = torch.rand(M, generator=g) / 100, torch.rand(N, generator=g) / 100
+    out.fill_(float("nan"))
+    moe.moe_int8_linear_lora(q.cuda(), qs.cuda(), w.cuda(), wsc.cuda(), lp, x.cuda(), ids.cuda(), out, ws)
+    base = (q[rows].double() @ w.double().T) * qs[rows].double()[:, None] * wsc.double()
+    check_rows(out[rows], base + d, err + 2.0 ** -22 * base.abs(), torch.bfloat16)
