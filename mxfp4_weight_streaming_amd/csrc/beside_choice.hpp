@@ -91,9 +91,11 @@ constexpr int64_t kLoraNearTiles = 32;         // of 256 channels
 // Of these, u by each workgroup itself (FUSED) saves a launch where it is little
 // work: 16 ranks or less, of a K that is walked in few steps (one token, rank 16,
 // K 2,560: 3.7 us against 5.4, 8,192: 7.7 against 9.0; rank 64, K 512: 9.8
-// against 6.2), and where most workgroups run at once (one step: 32 tokens of
-// 2,560 channels 4.8 us against 5.4, 64 5.8 against 5.6; two steps, 4,096
-// channels: 16 tokens 5.4 against 6.7 at 2,560, 32 tokens 7.5 against 6.9).
+// against 6.2), and where the workgroups are few: at one step 64 tokens of 2,560
+// channels are 5.6 us both ways and 6.2 against 9.4 where the host launches each
+// call, 128 8.3 against 6.2.  At two steps (4,096 features and channels) 16
+// tokens take 5.4 us against 6.7 and 32 7.5 against 6.9; where K is odd (769), 48
+// of 2,563 channels 9.2 against 7.1, 16 of 2,560 (K 2,563) 7.0 against 8.4.
 constexpr int kLoraStep = 2560;             // values of K that a wave asks for at once
 constexpr int64_t kLoraFusedDepth = 8192;
 
@@ -119,7 +121,7 @@ constexpr LoraPlan lora_plan(int64_t M, int64_t N, int64_t K, int r)
     const int64_t tn = ceil_div(N, 256), tm = ceil_div(M, 16);
     p.few = M * lora_padded(r) <= kLoraFewValues && M * r * (K + N) <= kLoraFewReads;
     p.near = tn >= kLoraNearTiles;
-    p.fused = p.few && r <= 16 && K >= 8 && K <= kLoraFusedDepth && M * tn <= (K <= kLoraStep ? 2 : 1) * kCus;
+    p.fused = p.few && r <= 16 && K >= 8 && K <= kLoraFusedDepth && M * tn <= (K <= kLoraStep && K % 2 == 0 ? 3 : 1) * kCus;
     p.shrink_slots = lora_slots(tm * ceil_div(r, r > 16 ? 32 : 16), kCus);
     p.expand_slots = lora_slots(tm * tn, 4 * kCus);
     return p;

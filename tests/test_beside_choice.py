@@ -72,7 +72,7 @@ def test_adapter_plans(choose):
 
 def test_adapter_tests_reach_every_kernel(choose):
     """The sizes of tests/test_gpu_lora.py: fused and not, few and many, with slots and without."""
-    got = choose("lora", [(1, 2560, 2560, 16), (64, 2560, 2560, 16), (9, 200, 96, 16), (1, 70, 130, 16), (300, 48, 64, 128),
+    got = choose("lora", [(1, 2560, 2560, 16), (70, 65, 257, 33), (9, 200, 96, 16), (1, 70, 130, 16), (300, 48, 64, 128),
                           (512, 1024, 2560, 64), (2048, 768, 512, 16), (130, 2563, 769, 100),
                           (16, 60000, 256, 64), (60, 3400, 3300, 128)])
     assert [g[0] for g in got[-2:]] == [0, 0]            # few tokens that would read too much by themselves
