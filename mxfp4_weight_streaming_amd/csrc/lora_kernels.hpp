@@ -586,9 +586,11 @@ __global__ __launch_bounds__(256) void lora_few_kernel(LoraArgs g)
         }
     }
     if (n >= g.N) return;
-    const float o = (g.base == nullptr ? 0.0f : BASE32 ? __uint_as_float(base) : bf16_bits_to_f32(base)) + d;
+    // (a token without an adapter keeps base's bits: -0 + 0 would be +0)
+    const uint32_t bits = g.base == nullptr ? 0 : base;
+    const float b = BASE32 ? __uint_as_float(bits) : bf16_bits_to_f32(bits), o = i >= 0 ? b + d : b;
     if constexpr (F32) static_cast<float*>(g.out)[at] = o;
-    else static_cast<uint16_t*>(g.out)[at] = (uint16_t)f32_to_bf16_bits(o);
+    else static_cast<uint16_t*>(g.out)[at] = (uint16_t)(BASE32 || i >= 0 ? f32_to_bf16_bits(o) : bits);
 }
 
 }  // namespace moe
