@@ -395,22 +395,27 @@ __device__ __forceinline__ Row4<F32> load_row4(const void* p, size_t at, int n)
 }
 
 template <bool F32>
-__device__ __forceinline__ void store_row4(void* p, size_t at, int n, const float (&v)[4])
+__device__ __forceinline__ Row4<F32> round_row4(const float (&v)[4])
+{
+    Row4<F32> r;
+#pragma unroll
+    for (int i = 0; i < (F32 ? 4 : 2); ++i)
+        r.d[i] = F32 ? __float_as_uint(v[i]) : f32_to_bf16_bits(v[2 * i]) | f32_to_bf16_bits(v[2 * i + 1]) << 16;
+    return r;
+}
+
+template <bool F32>
+__device__ __forceinline__ void store_row4(void* p, size_t at, int n, const Row4<F32>& v)
 {
     if (n >= 4) {
-        if constexpr (F32) {
-            *reinterpret_cast<f32x4_word*>(static_cast<float*>(p) + at) = f32x4{v[0], v[1], v[2], v[3]};
-        } else {
-            const u32x2 d = {f32_to_bf16_bits(v[0]) | f32_to_bf16_bits(v[1]) << 16,
-                             f32_to_bf16_bits(v[2]) | f32_to_bf16_bits(v[3]) << 16};
-            *reinterpret_cast<u32x2_half*>(static_cast<uint16_t*>(p) + at) = d;
-        }
+        if constexpr (F32) *reinterpret_cast<u32x4_word*>(static_cast<float*>(p) + at) = u32x4{v.d[0], v.d[1], v.d[2], v.d[3]};
+        else *reinterpret_cast<u32x2_half*>(static_cast<uint16_t*>(p) + at) = u32x2{v.d[0], v.d[1]};
     } else {
 #pragma unroll
         for (int i = 0; i < 3; ++i)
             if (i < n) {
-                if constexpr (F32) static_cast<float*>(p)[at + i] = v[i];
-                else static_cast<uint16_t*>(p)[at + i] = (uint16_t)f32_to_bf16_bits(v[i]);
+                if constexpr (F32) static_cast<uint32_t*>(p)[at + i] = v.d[i];
+                else static_cast<uint16_t*>(p)[at + i] = (uint16_t)(v.d[i >> 1] >> (16 * (i & 1)));
             }
     }
 }
@@ -481,10 +486,13 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs g)
     for (int e = 0; e < 4; ++e)
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[e][j] = base[e].get(j);
-    uint32_t own = 0;
+    uint32_t own = 0, bare = 0;
     each_adapter(id, slot, g.slots, [&](int i, uint32_t mask) {
         own |= mask;
-        if (i < 0) return;
+        if (i < 0) {
+            bare = mask;
+            return;
+        }
         if (i != held) load_b(held = i);
         f32x4 acc[4] = {};
 #pragma unroll
@@ -508,11 +516,18 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs g)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o[e][j] += mask >> (quarter * 4 + e) & 1 ? acc[j][e] : 0.0f;
+            for (int j = 0; j < 4; ++j) o[e][j] = mask >> (quarter * 4 + e) & 1 ? o[e][j] + acc[j][e] : o[e][j];
     });
+    // (a token without an adapter keeps base's bits, which nothing is added to and
+    // no rounding changes but from fp32 to bf16)
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-        if (own >> (quarter * 4 + e) & 1) store_row4<F32>(g.out, (size_t)(m0 + quarter * 4 + e) * g.N + n, left, o[e]);
+        if (own >> (quarter * 4 + e) & 1) {
+            Row4<F32> v = round_row4<F32>(o[e]);
+            if constexpr (BASE32 == F32)
+                if (bare >> (quarter * 4 + e) & 1) v = base[e];
+            store_row4<F32>(g.out, (size_t)(m0 + quarter * 4 + e) * g.N + n, left, v);
+        }
 }
 
 // ---------------------------------------------------------------------------

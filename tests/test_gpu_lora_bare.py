@@ -106,3 +106,19 @@ def _product(moe, M, L, r, K, N, dtype):
 @pytest.mark.parametrize("M,L,r,K,N", FEW)
 def test_few_tokens_with_the_product(moe, M, L, r, K, N, dtype):
     _product(moe, M, L, r, K, N, dtype)
+
+
+# on the matrix cores: ranks of less than 8, of one, two and four steps, with and without slots
+MANY = [(520, 3, 16, 64, 70), (520, 5, 3, 40, 33), (600, 20, 13, 72, 259), (300, 4, 64, 130, 65), (200, 3, 128, 96, 257), (2048, 40, 16, 64, 1030)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("M,L,r,K,N", MANY)
+def test_many_tokens(moe, M, L, r, K, N, dtype):
+    _check(moe, M, L, r, K, N, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("M,L,r,K,N", MANY)
+def test_many_tokens_with_the_product(moe, M, L, r, K, N, dtype):
+    _product(moe, M, L, r, K, N, dtype)
