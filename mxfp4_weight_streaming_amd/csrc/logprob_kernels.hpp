@@ -17,8 +17,11 @@
 // the largest is kept, and the K-th largest of 64 disjoint sets' maxima bounds
 // the K-th largest logit from below.  Only groups that reach the bound (24 for
 // K = 20 on average, 44 for K = 32) are read again, and what reaches it in them
-// is ranked by counting.  Rows where more than a list's worth reach the bound
-// (equal logits) take their alternatives one after another.
+// is ranked by counting.  Where more than a list's worth reach the bound, many
+// logits share its value: larger ones are ranked alike, and the first that equal
+// it are found from the row's start (64 rows of 157,184 fp32, all but a few at a
+// finite value, 20 alternatives: 68 us, and 37 of flat rows, where such rows
+// masked by -inf take 18; a pass for each alternative took 1,300).
 //
 // What bounds it: many long rows of fp32 the reads (2,048 of 157,184 with 5
 // alternatives 251 us, 5.1 TB/s; a second pass alone would cost as much again),
@@ -338,6 +341,7 @@ struct LogprobLds {
     double log_s;
     float m;
     int32_t n_groups, n_cands;
+    int32_t reached[32], equal[2][kWave];
     float best_x[T];
     int32_t best_i[T];
 };
@@ -482,42 +486,125 @@ __device__ __forceinline__ void finish_row(const LogprobArgs& g, int64_t m, cons
         for (int k = n_cands + tid; k < K; k += T) put(k, -inf, -1);
         return;
     }
-    // one after another: the first of those behind the last one
-    float x = inf;
-    int i = -1;
-    for (int k = 0; k < K; ++k) {
-        float bx = -inf;
-        int bi = -1;
-        if (k == 0 || i >= 0) {
-            for (int v = tid; v < g.V; v += T) {
-                const float c = logit_at(row, F32, (size_t)v);
-                if (c > -inf && logit_before(x, i, c, v) && (bi < 0 || logit_before(c, v, bx, bi))) {
+    // Too many reach the bound, which is a value that many logits share (masks of a
+    // finite value, flat rows).  The K-th largest of the groups' maxima itself, bit
+    // by bit from the top (of the order of -inf there are always K):
+    __syncthreads();
+    int id = tid;                                        // (made opaque: what follows from it would be kept through all rows, spilled)
+    asm volatile("" : "+v"(id));
+    const int at_lane = id & 63;
+    if (id < 32) lds.reached[id] = 0;
+    if (id == 0) lds.n_groups = lds.n_cands = 0;
+    for (int c = id; c < kLogprobCandidates; c += T) lds.cands[c] = 0;
+    __syncthreads();
+    uint32_t kth = 0;
+#pragma unroll 1
+    for (int bit = 31; bit >= 0; --bit) {
+        const uint32_t trial = kth | 1u << bit;
+        int n = 0;
+#pragma unroll
+        for (int c = 0; c < NG; c += 8)
+            if (c < rows)
+#pragma unroll
+                for (int i = c; i < c + 8; ++i) n += __popcll(__ballot(float_order(largest[i]) >= trial));
+        if (at_lane == 0 && n > 0) atomicAdd(&lds.reached[bit], n);
+        __syncthreads();
+        if (lds.reached[bit] >= K) kth = trial;
+    }
+    // Larger logits stand in groups of a larger maximum, of which there are fewer
+    // than K; they come first.
+#pragma unroll
+    for (int c = 0; c < NG; c += 8)
+        if (c < rows)
+#pragma unroll
+            for (int i = c; i < c + 8; ++i)
+                if (float_order(largest[i]) > kth) lds.groups[atomicAdd(&lds.n_groups, 1)] = i * T + id;
+    __syncthreads();
+    const int span = 16 * g.group_segments, n_read = lds.n_groups * span;
+    auto each_larger = [&](auto f) {
+        for (int j = id; j < n_read; j += T) {
+            const int group = lds.groups[j / span], in = j % span;
+            const int64_t p = ((int64_t)(group / TW) * g.group_segments + (in >> 4)) * (16 * TW) + (group % TW >> 6) * 1024 +
+                              logit_place<F32>(group & 63, in & 15);
+            if (p >= g.V) continue;
+            const float x = logit_at(row, F32, (size_t)p);
+            if (float_order(x) > kth) f(x, (int)p);
+        }
+    };
+    each_larger([&](float x, int p) {
+        const int at = atomicAdd(&lds.n_cands, 1);
+        if (at < kLogprobCandidates) lds.cands[at] = (uint64_t)float_order(x) << 32 | (uint32_t)~p;
+    });
+    __syncthreads();
+    const int larger = lds.n_cands;
+    if (larger <= kLogprobCandidates) {
+        for (int c = id; c < larger; c += T) {
+            const uint64_t own = lds.cands[c];
+            const int at = key_place(lds.cands, larger, own);
+            if (at < K) put(at, order_float((uint32_t)(own >> 32)), (int)~(uint32_t)own);
+        }
+    } else {
+        // (groups of several segments that are large throughout) one after another:
+        // the first of those behind the last one
+        float x = inf;
+        int i = -1;
+        for (int k = 0; k < K; ++k) {
+            float bx = -inf;
+            int bi = -1;
+            each_larger([&](float c, int v) {
+                if (logit_before(x, i, c, v) && (bi < 0 || logit_before(c, v, bx, bi))) {
                     bx = c;
                     bi = v;
                 }
-            }
+            });
             __syncthreads();
-            lds.best_x[tid] = bx;
-            lds.best_i[tid] = bi;
+            lds.best_x[id] = bx;
+            lds.best_i[id] = bi;
             __syncthreads();
             for (int half = T / 2; half > 0; half >>= 1) {
-                if (tid < half) {
-                    const float ox = lds.best_x[tid + half];
-                    const int oi = lds.best_i[tid + half];
-                    if (oi >= 0 && (lds.best_i[tid] < 0 || logit_before(ox, oi, lds.best_x[tid], lds.best_i[tid]))) {
-                        lds.best_x[tid] = ox;
-                        lds.best_i[tid] = oi;
+                if (id < half) {
+                    const float ox = lds.best_x[id + half];
+                    const int oi = lds.best_i[id + half];
+                    if (oi >= 0 && (lds.best_i[id] < 0 || logit_before(ox, oi, lds.best_x[id], lds.best_i[id]))) {
+                        lds.best_x[id] = ox;
+                        lds.best_i[id] = oi;
                     }
                 }
                 __syncthreads();
             }
-            bx = lds.best_x[0];
-            bi = lds.best_i[0];
+            x = lds.best_x[0];
+            i = lds.best_i[0];
+            if (id == 0) put(k, x, i);
         }
-        x = bx;
-        i = bi;
-        if (tid == 0) put(k, x, i);
+        return;
     }
+    // Then the first of those that equal it: 64 pieces of a wave's 64 logits at a
+    // time, counted, until there are enough.
+    constexpr int W = T / kWave, U = kWave / W;
+    const float tie = order_float(kth);
+    int found = larger;
+    for (int64_t at = 0, turn = 0; tie > -inf && at < g.V && found < K; at += U * T, turn ^= 1) {
+        uint64_t who[U];
+        float x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) x[u] = logit_at(row, F32, (size_t)min(at + u * T + id, (int64_t)g.V - 1));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            who[u] = __ballot(at + u * T + id < g.V && x[u] == tie);
+            if (at_lane == 0) lds.equal[turn][u * W + wave] = __popcll(who[u]);
+        }
+        __syncthreads();
+        const int mine = lds.equal[turn][at_lane];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (who[u] == 0) continue;
+            const int to = found + wave_sum_i32(at_lane < u * W + wave ? mine : 0) +
+                           (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(who[u] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who[u], 0));
+            if ((who[u] >> at_lane & 1) != 0 && to < K) put(to, tie, (int)(at + u * T + id));
+        }
+        found += wave_sum_i32(mine);
+    }
+    for (int k = found + id; k < K; k += T) put(k, -inf, -1);
 }
 
 // Walks the segments [s0, s1) of a row with the workgroup's T / 64 waves, 1,024
