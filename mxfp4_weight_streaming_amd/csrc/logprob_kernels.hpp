@@ -721,9 +721,10 @@ __global__ __launch_bounds__(kLogprobJoin) void logprob_join_kernel(LogprobArgs 
 // meanwhile, in two passes over the same row: one after the other they are two
 // chains of thousands of cycles (12 rows of 192: 7.0 us, with two waves 4.1, of
 // which the sums alone are 3.8; 4,096 of 1,000: 12 us).  ONE: a row of at most
-// 1,024 logits.
+// 1,024 logits; five workgroups a compute unit, as the rows with shared values
+// would otherwise take registers for four and cost all others 5%.
 template <bool F32, bool ONE>
-__global__ __launch_bounds__(256, 4) void logprob_short_kernel(LogprobArgs g)
+__global__ __launch_bounds__(256, ONE ? 5 : 4) void logprob_short_kernel(LogprobArgs g)
 {
     constexpr int E = Logits16<F32>::kVec;
     __shared__ uint32_t bests[2][64];
@@ -789,9 +790,9 @@ __global__ __launch_bounds__(256, 4) void logprob_short_kernel(LogprobArgs g)
             }
         }
     };
+    float best = -inf;
     if (row && alternatives) {
         if constexpr (ONE) w.load(0, raw);
-        float best = -inf;
         each([&](int) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) best = fmaxf(best, logit_value(raw.get(i)));   // (behind the row: -inf)
@@ -841,20 +842,80 @@ __global__ __launch_bounds__(256, 4) void logprob_short_kernel(LogprobArgs g)
         for (int k = n + lane; k < K; k += 64) put(k, 0);
         return;
     }
-    // (equal logits) the largest key below the last, K times
-    uint64_t last = ~0ull;
-    for (int k = 0; k < K; ++k) {
-        uint64_t top = 0;
-        each([&](int at) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const uint64_t key = key_of(at, i);
-                if (key < last) top = max_u64(top, key);
-            }
-        });
-        last = wave_max_u64(top);
-        if (lane == 0) put(k, last);
+    // Many share the bound's value: as in finish_row, with lanes for groups (1,024
+    // rows of 6,000, all but a few at a finite value, 20 alternatives: 31 us, where
+    // a pass for each took 152).
+    bests[slot][lane] = float_order(best);
+    __builtin_amdgcn_wave_barrier();
+    int before = 0;
+#pragma unroll 16
+    for (int l = 0; l < 64; ++l) {
+        const uint32_t other = bests[slot][l], mine = float_order(best);
+        before += other > mine || (other == mine && l < lane) ? 1 : 0;
     }
+    const uint32_t kth = (uint32_t)__builtin_amdgcn_readlane((int)float_order(best), (int)__builtin_ctzll(__ballot(before == K - 1)));
+#pragma unroll
+    for (int c = 0; c < kLogprobShortList; c += 64) cands[slot][c + lane] = 0;
+    __builtin_amdgcn_wave_barrier();
+    int larger = 0;
+    each([&](int at) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const uint64_t key = key_of(at, i), who = __ballot((uint32_t)(key >> 32) > kth);
+            if (who == 0) continue;
+            const int to = larger + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
+            if ((uint32_t)(key >> 32) > kth && to < kLogprobShortList) cands[slot][to] = key;
+            larger += __popcll(who);
+        }
+    });
+    __builtin_amdgcn_wave_barrier();
+    if (larger > kLogprobShortList) {
+        // (less than K lanes, but large throughout) the largest key below the last, K times
+        uint64_t last = ~0ull;
+        for (int k = 0; k < K; ++k) {
+            uint64_t top = 0;
+            each([&](int at) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const uint64_t key = key_of(at, i);
+                    if (key < last) top = max_u64(top, key);
+                }
+            });
+            last = wave_max_u64(top);
+            if (lane == 0) put(k, last);
+        }
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < kLogprobShortList; c += 64) {
+        const uint64_t key = cands[slot][c + lane];
+        const int to = c < larger ? key_place(cands[slot], larger, key) : K;
+        if (c + lane < larger && to < K) put(to, key);
+    }
+    int found = larger;
+    each([&](int at) {
+#pragma unroll
+        for (int u = 0; u < 16; u += E) {
+            if (found >= K) return;
+            int ahead = 0, all = 0;                      // that stand before the lane's own, and in all
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const uint64_t who = __ballot((uint32_t)(key_of(at, u + e) >> 32) == kth);
+                ahead += (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
+                all += __popcll(who);
+            }
+            if (all == 0) continue;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const uint64_t key = key_of(at, u + e);
+                if ((uint32_t)(key >> 32) != kth) continue;
+                if (found + ahead < K) put(found + ahead, key);
+                ++ahead;
+            }
+            found += all;
+        }
+    });
+    for (int k = found + lane; k < K; k += 64) put(k, 0);
 }
 
 }  // namespace moe

@@ -7,7 +7,7 @@ import torch
 
 from _around_gpu import Out
 from _beside_ref import Logprobs
-from _beside_sizes import LOGPROB_ROWS
+from _beside_sizes import LOGPROB_ROWS, LOGPROB_SHORT_ROWS
 
 pytestmark = pytest.mark.gpu
 
@@ -46,7 +46,7 @@ def kinds_of_rows(V, dtype, g):
     mixed[pick(3)], mixed[pick(3)], mixed[pick(40)] = INF, float("nan"), 30.0
     rows.append(mixed)
     t = torch.randint(0, V, (len(rows),), generator=g).to(torch.int32)
-    t[3], t[9], t[10], t[20] = int(rows[3].argmax()), V - 1, V - 1, V - 350
+    t[3], t[9], t[10], t[20] = int(rows[3].argmax()), V - 1, V - 1, max(V - 350, 0)
     t[11] = -1
     return torch.stack(rows).to(dtype), t
 
@@ -63,7 +63,7 @@ def call(moe, x, t, k):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("M,V", LOGPROB_ROWS)
+@pytest.mark.parametrize("M,V", LOGPROB_ROWS + LOGPROB_SHORT_ROWS)
 def test_rows_of_every_kind(moe, M, V, dtype):
     """As many rows as the split of the work is for, of some 30 kinds in turn; equal rows give equal bits."""
     g = torch.Generator().manual_seed(M + V)
@@ -129,3 +129,16 @@ def test_a_finite_mask_costs_no_multiple(moe, M, V, k, dtype):
     flat = _time(moe, torch.zeros(M, V, dtype=dtype, device="cuda"), k)
     print(f"flat {flat:.1f} us", flush=True)
     assert flat < 5 * plain + 20
+
+
+@pytest.mark.parametrize("M,V,dtype", [(1024, 6000, torch.float32), (512, 4096, torch.bfloat16), (1024, 2048, torch.float32)])
+def test_a_finite_mask_of_short_rows_costs_no_multiple(moe, M, V, dtype):
+    k = 32
+    g = torch.Generator(device="cuda").manual_seed(V)
+    x = torch.randn(M, V, generator=g, device="cuda")
+    keep = torch.rand(M, V, generator=g, device="cuda") < 1e-3
+    plain = _time(moe, torch.where(keep, x, -INF).to(dtype), k)
+    for rows in (torch.where(keep, x, torch.finfo(dtype).min).to(dtype), torch.zeros(M, V, dtype=dtype, device="cuda")):
+        masked = _time(moe, rows, k)
+        print(f"M={M} V={V} {dtype}: -inf {plain:.1f} us, others {masked:.1f} us", flush=True)
+        assert masked < 4 * plain
