@@ -538,9 +538,11 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs g)
 // channel, number (64 / L) (lane % L) + lane / L.  A row's last values are read
 // with those before them, which count once.  Workgroups of the same channels
 // follow one another, on one XCD where B is large (near).  FUSED: every workgroup
-// computes its token's u itself (A comes from L2 after the first), which saves a
-// launch: one token of rank 16, 2,560 to 2,560, 3.7 us, of which a launch is 1.6
-// and the rest ids, A and x, and the sums' reduction.  Four tokens and 157,184
+// computes its token's u itself, which saves a launch: one token of rank 16, 2,560
+// to 2,560, 3.6 us, of which a launch is 1.6 and the rest ids, A and x, and the
+// sums' reduction.  There a token's workgroups follow one another on an XCD, so
+// that A comes from its L2 after the first (in turn over all XCDs, by number, 51
+// tokens took 7.1 us where 48 took 4.7, now 4.6, and 25 of K 8,192 13.1, now 7.7).  Four tokens and 157,184
 // channels, 25.5 MB: 7.3 us with the launch before it, 3.5 TB/s.
 // ---------------------------------------------------------------------------
 template <bool BASE32, bool F32, bool FUSED, int L>
@@ -549,8 +551,10 @@ __global__ __launch_bounds__(256) void lora_few_kernel(LoraArgs g)
     __shared__ float us[kMaxLoraRank];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int part = lane % L, group = lane / L;
-    const uint32_t M = (uint32_t)g.M, tile = g.near ? tile_of(blockIdx.x, gridDim.x) : blockIdx.x;
-    const int64_t m = tile % M, n0 = (int64_t)(tile / M) * 256 + wave * 64, n = n0 + part * (64 / L) + group;
+    const uint32_t M = (uint32_t)g.M, tn = (uint32_t)((g.N + 255) / 256);
+    const uint32_t tile = FUSED || g.near ? tile_of(blockIdx.x, gridDim.x) : blockIdx.x;
+    const int64_t m = FUSED ? tile / tn : tile % M;
+    const int64_t n0 = (int64_t)(FUSED ? tile % tn : tile / M) * 256 + wave * 64, n = n0 + part * (64 / L) + group;
     const int i = __builtin_amdgcn_readfirstlane(adapter_of(g, m));
     const size_t at = (size_t)m * g.N + min(n, g.N - 1);
     // (asked for in any case, so that it is not waited for behind a branch)
