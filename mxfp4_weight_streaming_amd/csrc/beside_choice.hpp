@@ -88,16 +88,31 @@ constexpr int64_t kLoraFewReads = 48 << 20;    // values of A and B
 // against 5.6).
 constexpr int64_t kLoraNearTiles = 32;         // of 256 channels
 
-// Of these, u by each workgroup itself (FUSED) saves a launch where it is little
-// work: 16 ranks or less, of a K that is walked in few steps (one token, rank 16,
-// K 2,560: 3.7 us against 5.4, 8,192: 7.7 against 9.0; rank 64, K 512: 9.8
-// against 6.2), and where the workgroups are few: at one step 64 tokens of 2,560
-// channels are 5.6 us both ways and 6.2 against 9.4 where the host launches each
-// call, 128 8.3 against 6.2.  At two steps (4,096 features and channels) 16
-// tokens take 5.4 us against 6.7 and 32 7.5 against 6.9; where K is odd (769), 48
-// of 2,563 channels 9.2 against 7.1, 16 of 2,560 (K 2,563) 7.0 against 8.4.
+// Of these, u by each workgroup itself (FUSED, up to 16 ranks) saves a launch,
+// and costs every further workgroup of a compute unit its steps along K, twice
+// where K is odd (rows at any byte).  Two launches / one, us in a graph, an
+// adapter a token:
+//   workgroups a compute unit         1             2            3            4
+//   K 2,560 (and 64 to 2,558)     5.6 /  3.8    5.7 /  4.6   5.7 /  5.6   5.9 /  6.4
+//   ... rank 8                    5.1 /  3.7    5.3 /  4.4   5.2 /  5.2   5.5 /  5.8
+//   K 769, 1,281                  6.7 /  5.0    6.8 /  6.7   6.7 /  8.6
+//   K 4,096                       7.0 /  5.2    7.1 /  6.8   7.5 /  8.7
+//   ... rank 8                    6.3 /  5.2    6.4 /  6.7
+//   K 2,563                       8.7 /  7.0    8.8 / 10.3
+//   K 8,192                       9.3 /  7.6    9.4 / 10.0
+//   ... rank 8                    8.1 /  7.8    8.2 / 10.2
+//   K 7,681                      12.4 / 10.8   12.5 / 17.9
+//   ... rank 8                    9.3 / 11.7    9.6 / 19.8
+//   K 16,384                     12.3 / 10.8   13.8 / 16.2
+// Where the host launches each call, two take 8.0 at least and one 5.8, so what is
+// level in a graph is one.
 constexpr int kLoraStep = 2560;             // values of K that a wave asks for at once
-constexpr int64_t kLoraFusedDepth = 8192;
+
+constexpr bool lora_fused(int64_t workgroups, int64_t K, int r)
+{
+    const int64_t steps = ceil_div(K, kLoraStep) * (K % 2 == 0 ? 1 : 2), further = ceil_div(workgroups, kCus) - 1;
+    return r <= 16 && K >= 8 && steps <= (r > 8 ? 8 : 4) && further * steps <= (r > 8 || steps == 1 ? 2 : 0);
+}
 
 struct LoraPlan {
     bool few, fused, near;
@@ -121,7 +136,7 @@ constexpr LoraPlan lora_plan(int64_t M, int64_t N, int64_t K, int r)
     const int64_t tn = ceil_div(N, 256), tm = ceil_div(M, 16);
     p.few = M * lora_padded(r) <= kLoraFewValues && M * r * (K + N) <= kLoraFewReads;
     p.near = tn >= kLoraNearTiles;
-    p.fused = p.few && r <= 16 && K >= 8 && K <= kLoraFusedDepth && M * tn <= (K <= kLoraStep && K % 2 == 0 ? 3 : 1) * kCus;
+    p.fused = p.few && lora_fused(M * tn, K, r);
     p.shrink_slots = lora_slots(tm * ceil_div(r, r > 16 ? 32 : 16), kCus);
     p.expand_slots = lora_slots(tm * tn, 4 * kCus);
     return p;
