@@ -1,6 +1,6 @@
 """CPU-only: the sizes of the GPU tests in tests/_beside_sizes.py reach every
 kernel and every way of splitting a row, by the library's own rules."""
-from _beside_sizes import LOGPROB_ROWS, LOGPROB_SHORT_ROWS
+from _beside_sizes import LOGPROB_ROWS, LOGPROB_SHORT_ROWS, LORA_CHANNELS, LORA_DEPTHS, LORA_LARGE, LORA_RANKS
 from test_beside_choice import choose  # noqa: F401
 
 
@@ -32,3 +32,24 @@ def test_one_launch_for_few_tokens(choose):  # noqa: F811
         assert [fused(5, K, N) for K in (9, 769, 4096, 4095, 8192)] == [1.0] * 5
         assert [fused(8, K, N) for K in (7, 5121, 10242)] == [fused(16, K, N) for K in (7, 10241, 20482)] == [0.0] * 3
     assert fused(17, 64) == 0.0
+
+
+def test_adapters_of_many_tokens_reach_every_form(choose):  # noqa: F811
+    """All on the matrix cores; one and two tiles of ranks a workgroup, steps of 32 ranks, rows of B of less than 8 and of
+    no multiple of 8, depths below a load, below a step and between."""
+    sizes = LORA_RANKS + LORA_DEPTHS + LORA_CHANNELS + LORA_LARGE
+    got = choose("lora", [(M, N, K, r) for M, r, K, N in sizes])
+    assert all(g[0] == 0 for g in got)
+    # (two tiles, steps, less than 8, ending inside 8)
+    forms = lambda which: {(r > 16, 1 if r <= 32 else 2 if r <= 64 else 4, r < 8, r > 8 and r % 8 != 0) for _, r, _, _ in which}  # noqa: E731
+    every = {(False, 1, True, False), (False, 1, False, False), (False, 1, False, True), (True, 1, False, False), (True, 1, False, True),
+             (True, 2, False, False), (True, 2, False, True), (True, 4, False, False), (True, 4, False, True)}
+    assert forms(LORA_RANKS) == every
+    assert any(65 <= r <= 96 for _, r, _, _ in LORA_RANKS)   # four steps' kernel with three
+    for r in (13, 16, 40):
+        depths = {K for _, rank, K, _ in LORA_DEPTHS if rank == r}
+        assert {1, 7, 8, 9, 63, 64, 65} <= depths and any(K > 2560 for K in depths)
+    assert {N % 4 for _, _, _, N in LORA_CHANNELS} == {0, 1, 2, 3} and min(N for _, _, _, N in LORA_CHANNELS) == 1
+    assert {1} < {g[2] for g in got} and {1} < {g[3] for g in got}
+    large = choose("lora", [(M, N, K, r) for M, r, K, N in LORA_LARGE])
+    assert any(g[2] == 1 for g in large) and any(g[3] == 1 for g in large)
