@@ -518,9 +518,11 @@ size_t moe_lora_workspace_bytes(const moe_lora* lora, int32_t max_tokens);
  * i = adapter_ids[m]:
  *   u = scale[i] * (A[i] x[m])      products of bf16 values summed in fp32
  *   out[m] = base[m] + B[i] u       u and the sums fp32, rounded once to out_type
- * A token whose id is outside [0, num_adapters) has no adapter: out[m] = base[m].
- * What a row becomes depends on its own token and adapter alone.  A weight that
- * is infinite may give NaN where the formula gives an infinity.
+ * A token whose id is outside [0, num_adapters) has no adapter: out[m] = base[m],
+ * bit for bit (0 without a base).  What a row becomes depends on its own token, its
+ * adapter and the call's sizes, not on the other tokens or its place among them; a
+ * call of another M may add the same sums up in another order.  A weight that is
+ * infinite may give NaN where the formula gives an infinity.
  * x [M,K] bf16 (the projection's input), adapter_ids [M] int32 in any order,
  * base [M,N] of out_type, or NULL (0); out [M,N], may be base itself.  x, base
  * and out are 16-byte aligned. */

@@ -79,10 +79,14 @@ hipError_t shrink(LoraArgs a, const LoraPlan& p, hipStream_t s)
     return hipGetLastError();
 }
 
+// The rows of a that stand among `M` of a call.
 template <bool BASE32, bool F32>
-hipError_t add(const LoraArgs& a, hipStream_t s)
+hipError_t add(const LoraArgs& a, int64_t M, hipStream_t s)
 {
-    const LoraPlan p = lora_plan(a.M, a.N, a.K, a.r);
+    LoraPlan p = lora_plan(a.M, a.N, a.K, a.r);
+    // (a row's sums have one order wherever it stands among them)
+    p.few = lora_plan(M, a.N, a.K, a.r).few;
+    p.fused = p.few && p.fused;
     if (p.fused) return few<BASE32, F32, true>(a, p, s);
     const hipError_t e = shrink(a, p, s);
     if (e != hipSuccess) return e;
@@ -101,7 +105,7 @@ size_t lora_product_workspace(int64_t M, int64_t N, int r)
 hipError_t launch_lora_add(const LoraArgs& a, hipStream_t s)
 {
     if (!fits(a)) return hipErrorInvalidConfiguration;
-    return a.out_type == kTypeF32 ? add<true, true>(a, s) : add<false, false>(a, s);
+    return a.out_type == kTypeF32 ? add<true, true>(a, a.M, s) : add<false, false>(a, a.M, s);
 }
 
 // The product in fp32 first, into out where that is fp32 and else into the
@@ -129,7 +133,7 @@ hipError_t launch_int8_linear_lora(const Int8Args& p, const LoraArgs& a, hipStre
         g.out_type = kTypeF32;
         hipError_t e = launch_int8_linear(g, s);
         if (e != hipSuccess) return e;
-        e = f32 ? add<true, true>(l, s) : add<true, false>(l, s);
+        e = f32 ? add<true, true>(l, a.M, s) : add<true, false>(l, a.M, s);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;

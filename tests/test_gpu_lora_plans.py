@@ -151,6 +151,44 @@ def test_u_is_not_rounded(moe, M, r):
     assert torch.equal(out.t.cpu(), want)
 
 
+@pytest.mark.parametrize("r", [3, 13, 16, 40, 128])
+@pytest.mark.parametrize("M", [12, 60, 200, 600, 1100])
+def test_a_row_does_not_depend_on_its_place(moe, M, r):
+    """Tokens that occur several times among others give the same bits everywhere."""
+    g = torch.Generator().manual_seed(M + r)
+    L, K, N = 4, 300, 131
+    lp = moe.lora(torch.randn(L, r, K, generator=g).to(BF).cuda(), torch.randn(L, N, r, generator=g).to(BF).cuda(),
+                  torch.rand(L, generator=g).cuda())
+    x, ids, y = torch.randn(M, K, generator=g).to(BF), _ids(g, M, L), torch.randn(M, N, generator=g)
+    q = torch.randint(-127, 128, (M, K), generator=g).to(torch.int8)
+    qs, w, ws = torch.rand(M, generator=g), torch.randint(-127, 128, (N, K), generator=g).to(torch.int8), torch.rand(N, generator=g)
+    source = torch.where(torch.rand(M, generator=g) < 0.5, torch.randint(0, 5, (M,), generator=g), torch.arange(M))
+    source[:5] = torch.arange(5)                         # (those that are repeated are themselves)
+    x, ids, y, q, qs = (t[source].cuda() for t in (x, ids, y, q, qs))
+    scratch = moe.lora_workspace(lp, M)
+    for dtype in (F32, BF):
+        out = torch.empty(M, N, dtype=dtype, device="cuda")
+        moe.moe_lora_add(lp, x, ids, y.to(dtype), out, scratch)
+        assert torch.equal(out, out[source.cuda()])
+        moe.moe_int8_linear_lora(q, qs, w.cuda(), ws.cuda(), lp, x, ids, out, scratch)
+        assert torch.equal(out, out[source.cuda()])
+
+
+def test_a_row_does_not_depend_on_its_piece(moe):
+    """Rows of the int8 product that are taken some at a time: the last, fewer ones as the others."""
+    g = torch.Generator().manual_seed(9)
+    M, N, K, L, r = 520, 300000, 24, 3, 8                # 256, 256 and 8 rows
+    lp = moe.lora(torch.randn(L, r, K, generator=g).to(BF).cuda(), torch.randn(L, N, r, generator=g).to(BF).cuda())
+    q, w = (torch.randint(-127, 128, s, generator=g).to(torch.int8).cuda() for s in ((M, K), (N, K)))
+    qs, ws = torch.rand(M, generator=g).cuda() / 1000, torch.rand(N, generator=g).cuda() / 1000
+    x, ids = torch.randn(M, K, generator=g).to(BF).cuda(), torch.randint(-1, L, (M,), generator=g).to(torch.int32).cuda()
+    for t in (q, qs, x, ids):
+        t[512:] = t[:8]
+    out = torch.empty(M, N, dtype=BF, device="cuda")
+    moe.moe_int8_linear_lora(q, qs, w, ws, lp, x, ids, out, moe.lora_workspace(lp, M))
+    assert torch.equal(out[512:], out[:8])
+
+
 def _time(moe, M, r, K, N):
     """Microseconds of a call in a graph, an adapter a token."""
     g = torch.Generator(device="cuda").manual_seed(M)
