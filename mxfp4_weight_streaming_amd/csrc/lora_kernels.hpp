@@ -518,16 +518,24 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs g)
 #pragma unroll
             for (int j = 0; j < 4; ++j) o[e][j] = mask >> (quarter * 4 + e) & 1 ? o[e][j] + acc[j][e] : o[e][j];
     });
-    // (a token without an adapter keeps base's bits, which nothing is added to and
-    // no rounding changes but from fp32 to bf16)
+    Row4<F32> v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = round_row4<F32>(o[e]);
+    // (a token without an adapter keeps base's bits: nothing was added to them, and
+    // bf16's are the upper halves that they were, where rounding would change a
+    // signalling NaN)
+    if constexpr (!BASE32 && !F32)
+        if (bare != 0)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t same = __float_as_uint(o[e][2 * i]) >> 16 | (__float_as_uint(o[e][2 * i + 1]) & 0xFFFF0000u);
+                    v[e].d[i] = bare >> (quarter * 4 + e) & 1 ? same : v[e].d[i];
+                }
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-        if (own >> (quarter * 4 + e) & 1) {
-            Row4<F32> v = round_row4<F32>(o[e]);
-            if constexpr (BASE32 == F32)
-                if (bare >> (quarter * 4 + e) & 1) v = base[e];
-            store_row4<F32>(g.out, (size_t)(m0 + quarter * 4 + e) * g.N + n, left, v);
-        }
+        if (own >> (quarter * 4 + e) & 1) store_row4<F32>(g.out, (size_t)(m0 + quarter * 4 + e) * g.N + n, left, v[e]);
 }
 
 // ---------------------------------------------------------------------------
