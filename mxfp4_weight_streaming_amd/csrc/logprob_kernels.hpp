@@ -20,7 +20,7 @@
 // is ranked by counting.  Where more than a list's worth reach the bound, many
 // logits share its value: larger ones are ranked alike, and the first that equal
 // it are found from the row's start (64 rows of 157,184 fp32, all but a few at a
-// finite value, 20 alternatives: 68 us, and 37 of flat rows, where such rows
+// finite value, 20 alternatives: 40 us, and 37 of flat rows, where such rows
 // masked by -inf take 18; a pass for each alternative took 1,300).
 //
 // What bounds it: many long rows of fp32 the reads (2,048 of 157,184 with 5
@@ -498,6 +498,7 @@ __device__ __forceinline__ void finish_row(const LogprobArgs& g, int64_t m, cons
     for (int c = id; c < kLogprobCandidates; c += T) lds.cands[c] = 0;
     __syncthreads();
     uint32_t kth = 0;
+    int at_least = 0;                                    // groups whose maximum is that or more
 #pragma unroll 1
     for (int bit = 31; bit >= 0; --bit) {
         const uint32_t trial = kth | 1u << bit;
@@ -509,18 +510,24 @@ __device__ __forceinline__ void finish_row(const LogprobArgs& g, int64_t m, cons
                 for (int i = c; i < c + 8; ++i) n += __popcll(__ballot(float_order(largest[i]) >= trial));
         if (at_lane == 0 && n > 0) atomicAdd(&lds.reached[bit], n);
         __syncthreads();
-        if (lds.reached[bit] >= K) kth = trial;
+        if (lds.reached[bit] >= K) {
+            kth = trial;
+            at_least = lds.reached[bit];
+        }
     }
     // Larger logits stand in groups of a larger maximum, of which there are fewer
-    // than K; they come first.
+    // than K; they come first.  Where the groups that reach it are few, too (it is
+    // one of the logits that few are left of), those that equal it come with them.
+    const int span = 16 * g.group_segments;
+    const uint32_t above = (int64_t)at_least * span <= kLogprobCandidates ? kth - 1 : kth;
 #pragma unroll
     for (int c = 0; c < NG; c += 8)
         if (c < rows)
 #pragma unroll
             for (int i = c; i < c + 8; ++i)
-                if (float_order(largest[i]) > kth) lds.groups[atomicAdd(&lds.n_groups, 1)] = i * T + id;
+                if (float_order(largest[i]) > above) lds.groups[atomicAdd(&lds.n_groups, 1)] = i * T + id;
     __syncthreads();
-    const int span = 16 * g.group_segments, n_read = lds.n_groups * span;
+    const int n_read = lds.n_groups * span;
     auto each_larger = [&](auto f) {
         for (int j = id; j < n_read; j += T) {
             const int group = lds.groups[j / span], in = j % span;
@@ -528,7 +535,7 @@ __device__ __forceinline__ void finish_row(const LogprobArgs& g, int64_t m, cons
                               logit_place<F32>(group & 63, in & 15);
             if (p >= g.V) continue;
             const float x = logit_at(row, F32, (size_t)p);
-            if (float_order(x) > kth) f(x, (int)p);
+            if (float_order(x) > above) f(x, (int)p);
         }
     };
     each_larger([&](float x, int p) {

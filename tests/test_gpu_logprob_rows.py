@@ -36,6 +36,10 @@ def kinds_of_rows(V, dtype, g):
     flat = torch.full((V,), -2.0)                        # fewer larger than any topk but 32, and the rest alike
     flat[pick(19)] = 1.0 + torch.arange(19.0) / 8
     rows.append(flat)
+    for n in (22, 40):                                   # a few more left than 20 and 32, some of them in one lane's shares
+        flat = torch.full((V,), torch.finfo(dtype).min)
+        flat[pick(n)] = torch.randn(n, generator=g)
+        rows.append(flat)
     # all logits of 24 threads' shares large (whatever the workgroup's size and type): more than are ranked at
     # once where a share is of two segments; the rest alike
     for threads, each in ((256, 4), (512, 4), (1024, 4), (256, 8), (512, 8), (1024, 8)):
