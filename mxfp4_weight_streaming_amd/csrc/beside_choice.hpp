@@ -75,10 +75,14 @@ constexpr int lora_padded(int r) { return (r + 31) / 32 * 32; }   // ranks of a 
 // matrix cores tokens of one adapter share its rows, but a tile of 16 tokens takes
 // its adapters in turn.  K = N = 2,560, rank 16, us of few tokens / matrix cores:
 //   tokens        64          128         256         512         1,024
-//   an adapter    5.6 /  8.2  6.2 /  8.0  7.4 /  8.1 10.3 /  8.6  15.8 /  9.5
-//   one for 16    5.7 /  8.2  6.2 /  8.6  7.3 /  9.5 12.0 / 11.3  19.5 / 14.4
-//   one each      5.7 / 11.4  6.2 / 14.5 11.4 / 18.3 13.4 / 26.3  19.1 / 40.3
-// and 117 tokens of rank 64, 6,863 features and 8,388 channels (228 MB) 25 / 21.
+//   an adapter    5.7 /  8.0  6.1 /  8.0  7.4 /  8.1 10.2 /  8.5  15.9 /  9.6
+//   one for 16    5.8 /  8.0  6.1 /  8.0  7.3 /  8.2 12.9 /  8.6  21.6 /  9.6
+//   one each      5.6 / 11.5  6.1 / 14.6 11.5 / 18.4 17.6 / 25.8  29.8 / 39.6
+// (1,024 tokens of 8 adapters in any order: 19 on the matrix cores.)  By what they
+// read, an adapter / one for 16 / one each:
+//   60 tokens, rank 128, 3,300 to 3,400 (103 MB)  11.8 / 12.3  11.7 / 12.6  21.6 / 30.4
+//   120, rank 128, 2,560 to 2,560 (157 MB)        11.9 / 10.0  15.4 / 10.2  27.2 / 36.2
+//   250, rank 64, 4,096 to 4,096 (262 MB)         18.9 / 11.2  22.1 / 12.0  43.7 / 45.7
 constexpr int64_t kLoraFewValues = 16384;      // tokens times their padded rank
 constexpr int64_t kLoraFewReads = 48 << 20;    // values of A and B
 

@@ -25,9 +25,11 @@
 //
 // What bounds it: many long rows of fp32 the reads (2,048 of 157,184 with 5
 // alternatives 251 us, 5.1 TB/s; a second pass alone would cost as much again),
-// of bf16 the vector instructions (159 us; 16 logits of a lane are some 120 of
-// them and 16 exponentials); few rows and short ones chains of latencies: one row
-// of 157,184 is a launch, 3.3 us for its parts, a launch and 3 us to join them.
+// of bf16 the vector instructions more than anything else (159 us, 4.0 TB/s: 16
+// logits of a lane are some 190 of them, 16 of these exponentials, and take two
+// thirds of the issue slots, at three waves a SIMD); few rows and short ones
+// chains of latencies: one row of 157,184 is a launch, 3.3 us for its parts, a
+// launch and 3 us to join them.
 #pragma once
 
 #include <type_traits>
@@ -224,10 +226,12 @@ struct LogitWalk {
         }
     }
 
-    // Adds the 1,024 logits from `at`; returns the lane's largest.  The logits
-    // stay as they are: the maxima pass over NaN, which the clamp of a distance
-    // takes to e^-256 = 0 as it does -inf; an infinite one is put right where
-    // it is met as the largest.
+    // Adds the 1,024 logits from `at`; returns the lane's largest.  Exponentials
+    // and the sums of 16 are fp32, some 80 of 190 instructions as it is: a term at
+    // a distance d from the largest is off by 2^-24 (2.5 |d| + 24) of itself, which
+    // is what log S is allowed.  The logits stay as they are: the maxima pass over
+    // NaN, which the clamp of a distance takes to e^-256 = 0 as it does -inf; an
+    // infinite one is put right where it is met as the largest.
     __device__ __forceinline__ float add(int at, const Logits16<F32>& raw)
     {
         const float inf = __builtin_inff();
