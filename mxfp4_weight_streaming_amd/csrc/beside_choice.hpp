@@ -110,7 +110,11 @@ constexpr int64_t kLoraNearTiles = 32;         // of 256 channels
 //   K 16,384                     12.3 / 10.8   13.8 / 16.2
 // Where the host launches each call, two take 8.0 at least and one 5.8, so what is
 // level in a graph is one.
-constexpr int kLoraStep = 2560;             // values of K that a wave asks for at once
+// Values of K that a wave asks for at once, five loads a row: the layer's own
+// hidden size in one step.  Steps of 2,048 / of 2,560, one token of rank 16: K 1,024
+// 3.5 / 3.8 us, 2,048 3.3 / 3.8, 2,560 4.4 / 3.6, 4,096 4.3 / 5.0, 5,120 5.4 / 4.8,
+// 8,192 6.0 / 7.2; steps of 4,096: 4.7 up to 2,560, 4.5 at 4,096.
+constexpr int kLoraStep = 2560;
 
 constexpr bool lora_fused(int64_t workgroups, int64_t K, int r)
 {
